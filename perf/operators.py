@@ -171,7 +171,7 @@ def prepare(case, seed):
         s["gu"] = d.rows(T, C, torch.bfloat16)
         if own:
             import birkhoff_projection_amd as bp
-            s["workspace"] = bp.layer_workspace(T, C, s["x"].device)
+            s["workspace"] = bp.layer_ckpt_workspace(T, C, s["x"].device)
     elif op == "quant":
         s["x"] = d.activations(case["R"], case["C"], _dtype(case["dtype"]))
     elif op == "matmul":
