@@ -35,6 +35,12 @@ class LayerArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_int64)]
 
 
+class LayerCkpt(ctypes.Structure):
+    """Mirror of ``mhc_layer_ckpt``."""
+    _fields_ = [("format", ctypes.c_int32), ("x_codes", c_void_p), ("x_scales", c_void_p),
+                ("f_codes", c_void_p), ("f_scales", c_void_p)]
+
+
 # name -> (restype, argtypes), exactly as declared in include/mhc.h
 SIGNATURES = {
     "mhc_proj_opts_default": (c_int32, [ctypes.POINTER(ProjOpts)]),
@@ -59,6 +65,24 @@ SIGNATURES = {
     "mhc_layer_fwd": (c_int32, [ctypes.POINTER(LayerArgs), c_void_p]),
     "mhc_layer_bwd": (c_int32, [ctypes.POINTER(LayerArgs), c_void_p]),
     "mhc_layer_bwd_noalloc": (c_int32, [ctypes.POINTER(LayerArgs), c_void_p]),
+    "mhc_ckpt_pack": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_int32,
+                                c_void_p]),
+    "mhc_ckpt_unpack": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64, c_int32,
+                                  c_void_p]),
+    "mhc_stream_mix_ckpt": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                      c_int64, c_int32, c_int64, c_int32, ctypes.POINTER(ProjOpts),
+                                      c_void_p]),
+    "mhc_stream_mix_bwd_ckpt": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                          c_void_p, c_int64, c_int32, c_int64, c_int32, c_void_p]),
+    "mhc_layer_fwd_ckpt": (c_int32, [ctypes.POINTER(LayerArgs), ctypes.POINTER(LayerCkpt),
+                                     c_void_p]),
+    "mhc_layer_ckpt_workspace_bytes": (c_int64, [c_int64, c_int32, c_int64]),
+    "mhc_layer_bwd_ckpt": (c_int32, [ctypes.POINTER(LayerArgs), ctypes.POINTER(LayerCkpt),
+                                     c_void_p]),
+    "mhc_mx4_quantize": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64,
+                                   c_int32, c_void_p]),
+    "mhc_mx4_dequantize": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64,
+                                     c_void_p]),
     "mhc_status_string": (ctypes.c_char_p, [c_int32]),
     "mhc_last_error": (ctypes.c_char_p, []),
     "mhc_abi_version": (c_int32, []),

@@ -7,6 +7,8 @@
 
 #include "../../include/mhc.h"
 #include "kernels.h"
+#include "mxfmt.h"
+#include "qkernels.h"
 
 namespace {
 
@@ -480,6 +482,263 @@ mhc_status mhc_layer_bwd_noalloc(const mhc_layer_args* a, void* stream)
     if (e != hipSuccess) return launched(e, "layer_bwd_noalloc: scratch address");
     return launched(mhc::launch_layer_bwd(layer_bwd_ptrs(a, ws), a->T, a->C, (hipStream_t)stream),
                     "layer_bwd_noalloc launch");
+}
+
+// ---------------------------------------------------------------------------
+// Checkpoints in 8 bits
+// ---------------------------------------------------------------------------
+
+static_assert((int)MHC_CKPT_E4M3 == (int)mhc::kE4M3 && (int)MHC_CKPT_INT8 == (int)mhc::kInt8,
+              "header and kernels agree on the formats");
+
+namespace {
+
+// Largest number of 8-column chunks (rows padded to whole blocks of 32) one
+// pack or unpack call takes: 1024 chunks per workgroup of 256 work-items keep
+// the grid below 2^32 work-items.
+constexpr int64_t kMaxChunks = ((int64_t)1 << 33);
+
+int64_t blocks_of(int64_t C) { return (C + mhc::kMxBlock - 1) / mhc::kMxBlock; }
+
+mhc_status check_format(int32_t format)
+{
+    if (format != MHC_CKPT_E4M3 && format != MHC_CKPT_INT8)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "format must be 0 (e4m3) or 1 (int8), got %d", format);
+    return MHC_OK;
+}
+
+mhc_status check_dtype(int32_t dtype)
+{
+    if (dtype != MHC_BF16 && dtype != MHC_FP32)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "dtype must be 0 (bf16) or 1 (fp32), got %d", dtype);
+    return MHC_OK;
+}
+
+// R rows of C values, C a multiple of `step`
+mhc_status check_matrix(int64_t R, int64_t C, int64_t step)
+{
+    if (C < step || C % step != 0 || C > ((int64_t)1 << 30))
+        return fail(MHC_ERR_INVALID_ARGUMENT, "C must be a positive multiple of %lld (got %lld)",
+                    (long long)step, (long long)C);
+    if (R < 0 || R > kMaxChunks / (4 * blocks_of(C)))
+        return fail(MHC_ERR_INVALID_ARGUMENT, "R=%lld out of range for C=%lld", (long long)R, (long long)C);
+    return MHC_OK;
+}
+
+size_t dtype_bytes(int32_t dtype) { return dtype == MHC_FP32 ? 4 : 2; }
+
+mhc_status check_mix_shape(int64_t T, int32_t n, int64_t C)
+{
+    if (n != 4) return fail(MHC_ERR_UNSUPPORTED, "only n = 4 streams are supported (got %d)", n);
+    if (T < 0 || T > kMaxTokens) return fail(MHC_ERR_INVALID_ARGUMENT, "T=%lld out of range", (long long)T);
+    if (C < 8 || C % 8 != 0 || C > ((int64_t)1 << 30))
+        return fail(MHC_ERR_INVALID_ARGUMENT, "C must be a positive multiple of 8 (got %lld)", (long long)C);
+    return MHC_OK;
+}
+
+}  // namespace
+
+mhc_status mhc_ckpt_pack(const void* x, int32_t dtype, void* codes, uint8_t* scales, int64_t R,
+                         int64_t C, int32_t format, void* stream)
+{
+    mhc_status s;
+    if ((s = check_dtype(dtype)) != MHC_OK || (s = check_format(format)) != MHC_OK ||
+        (s = check_matrix(R, C, 8)) != MHC_OK)
+        return s;
+    if (R == 0) return ok();
+    const Buf b[] = {{x, (size_t)R * (size_t)C * dtype_bytes(dtype), "x"},
+                     {codes, (size_t)R * (size_t)C, "codes"},
+                     {scales, (size_t)R * (size_t)blocks_of(C), "scales"}};
+    if ((s = check_buffers(b, 3)) != MHC_OK) return s;
+    return launched(mhc::launch_ckpt_pack(x, dtype == MHC_FP32, mhc::Packed{codes, scales}, R, C,
+                                          format, (hipStream_t)stream),
+                    "ckpt_pack launch");
+}
+
+mhc_status mhc_ckpt_unpack(const void* codes, const uint8_t* scales, void* x, int32_t dtype,
+                           int64_t R, int64_t C, int32_t format, void* stream)
+{
+    mhc_status s;
+    if ((s = check_dtype(dtype)) != MHC_OK || (s = check_format(format)) != MHC_OK ||
+        (s = check_matrix(R, C, 8)) != MHC_OK)
+        return s;
+    if (R == 0) return ok();
+    const Buf b[] = {{codes, (size_t)R * (size_t)C, "codes"},
+                     {scales, (size_t)R * (size_t)blocks_of(C), "scales"},
+                     {x, (size_t)R * (size_t)C * dtype_bytes(dtype), "x"}};
+    if ((s = check_buffers(b, 3)) != MHC_OK) return s;
+    const mhc::Packed in{const_cast<void*>(codes), const_cast<uint8_t*>(scales)};
+    return launched(mhc::launch_ckpt_unpack(in, x, dtype == MHC_FP32, R, C, format,
+                                            (hipStream_t)stream),
+                    "ckpt_unpack launch");
+}
+
+mhc_status mhc_stream_mix_ckpt(const void* x, const float* H_or_logits, float* H_out, void* out,
+                               void* codes, uint8_t* scales, int64_t T, int32_t n, int64_t C,
+                               int32_t format, const mhc_proj_opts* proj, void* stream)
+{
+    mhc_status s;
+    if ((s = check_mix_shape(T, n, C)) != MHC_OK || (s = check_format(format)) != MHC_OK) return s;
+    mhc::SolverOpts o{};
+    if (proj != nullptr && (s = check_opts(proj, &o)) != MHC_OK) return s;
+    if (T == 0) return ok();
+    const size_t rows = (size_t)T * 4, hbytes = (size_t)T * 64;
+    const bool alias = proj != nullptr && H_out == H_or_logits;  // H over its own logits
+    const Buf b[] = {{x, rows * (size_t)C * 2, "x"},
+                     {H_or_logits, hbytes, "H_or_logits"},
+                     {out, rows * (size_t)C * 2, "out"},
+                     {codes, rows * (size_t)C, "codes"},
+                     {scales, rows * (size_t)blocks_of(C), "scales"},
+                     {H_out, hbytes, "H_out"}};
+    const bool has_H = proj != nullptr && H_out != nullptr && !alias;
+    if ((s = check_buffers(b, has_H ? 6 : 5)) != MHC_OK) return s;
+    return launched(mhc::launch_stream_mix_ckpt(x, H_or_logits, proj ? H_out : nullptr, out,
+                                                mhc::Packed{codes, scales}, T, C, format,
+                                                proj ? &o : nullptr, (hipStream_t)stream),
+                    "stream_mix_ckpt launch");
+}
+
+mhc_status mhc_stream_mix_bwd_ckpt(const void* codes, const uint8_t* scales, const float* H,
+                                   const void* grad_out, void* grad_x, float* grad_H, int64_t T,
+                                   int32_t n, int64_t C, int32_t format, void* stream)
+{
+    mhc_status s;
+    if ((s = check_mix_shape(T, n, C)) != MHC_OK || (s = check_format(format)) != MHC_OK) return s;
+    if (T == 0) return ok();
+    const size_t rows = (size_t)T * 4, hbytes = (size_t)T * 64;
+    const Buf b[] = {{codes, rows * (size_t)C, "codes"},
+                     {scales, rows * (size_t)blocks_of(C), "scales"},
+                     {H, hbytes, "H"},
+                     {grad_out, rows * (size_t)C * 2, "grad_out"},
+                     {grad_x, rows * (size_t)C * 2, "grad_x"},
+                     {grad_H, hbytes, "grad_H"}};
+    if ((s = check_buffers(b, 6)) != MHC_OK) return s;
+    const mhc::Packed in{const_cast<void*>(codes), const_cast<uint8_t*>(scales)};
+    return launched(mhc::launch_stream_mix_bwd_ckpt(in, H, grad_out, grad_x, grad_H, T, C, format,
+                                                    (hipStream_t)stream),
+                    "stream_mix_bwd_ckpt launch");
+}
+
+mhc_status mhc_layer_fwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* k, void* stream)
+{
+    if (a == nullptr || k == nullptr) return fail(MHC_ERR_INVALID_ARGUMENT, "args or ckpt is NULL");
+    mhc_status s = check_layer_shape(a->T, a->n, a->C);
+    if (s != MHC_OK || (s = check_format(k->format)) != MHC_OK) return s;
+    if (!(a->eps > 0.f) || !(a->eps < 1.f)) return fail(MHC_ERR_INVALID_ARGUMENT, "eps must be in (0, 1)");
+    mhc::SolverOpts o;
+    s = check_opts(a->proj, &o);
+    if (s != MHC_OK) return s;
+    if (a->T == 0) return ok();
+    const size_t T = (size_t)a->T, C = (size_t)a->C;
+    const Buf b[] = {{a->x, T * 4 * C * 2, "x"},
+                     {a->W, 24 * 4 * C * 2, "W"},
+                     {a->f, T * C * 2, "f"},
+                     {a->u, T * C * 2, "u"},
+                     {a->x_out, T * 4 * C * 2, "x_out"},
+                     {a->rms, T * 4, "rms"},
+                     {a->logits, T * 96, "logits"},
+                     {a->H_pre, T * 16, "H_pre"},
+                     {a->H_post, T * 16, "H_post"},
+                     {a->H_res, T * 64, "H_res"},
+                     {k->x_codes, T * 4 * C, "x_codes"},
+                     {k->x_scales, T * 4 * (C / 32), "x_scales"},
+                     {k->f_codes, T * C, "f_codes"},
+                     {k->f_scales, T * (C / 32), "f_scales"}};
+    s = check_buffers(b, sizeof(b) / sizeof(b[0]));
+    if (s != MHC_OK) return s;
+    const mhc::LayerPtrs p{a->x,   a->W,      a->f,     a->u,     a->x_out, a->rms,
+                           a->logits, a->H_pre, a->H_post, a->H_res, nullptr, nullptr,
+                           nullptr, nullptr,  nullptr,  nullptr,  nullptr};
+    return launched(mhc::launch_layer_fwd_ckpt(p, mhc::Packed{k->x_codes, k->x_scales},
+                                               mhc::Packed{k->f_codes, k->f_scales}, a->T, a->C,
+                                               a->eps, k->format, o, (hipStream_t)stream),
+                    "layer_fwd_ckpt launch");
+}
+
+int64_t mhc_layer_ckpt_workspace_bytes(int64_t T, int32_t n, int64_t C)
+{
+    if (check_layer_shape(T, n, C) != MHC_OK) return -1;
+    return mhc::layer_ckpt_plan(T, C).bytes;
+}
+
+mhc_status mhc_layer_bwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* k, void* stream)
+{
+    if (a == nullptr || k == nullptr) return fail(MHC_ERR_INVALID_ARGUMENT, "args or ckpt is NULL");
+    mhc_status s = check_layer_shape(a->T, a->n, a->C);
+    if (s != MHC_OK || (s = check_format(k->format)) != MHC_OK) return s;
+    if (a->T == 0) return ok();
+    const int64_t need = mhc::layer_ckpt_plan(a->T, a->C).bytes;
+    if (a->workspace_bytes < need)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "workspace_bytes=%lld < %lld required",
+                    (long long)a->workspace_bytes, (long long)need);
+    if (((uintptr_t)a->workspace & 255u) != 0)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+    const size_t T = (size_t)a->T, C = (size_t)a->C;
+    const Buf b[] = {{a->W, 24 * 4 * C * 2, "W"},
+                     {a->rms, T * 4, "rms"},
+                     {a->logits, T * 96, "logits"},
+                     {a->H_pre, T * 16, "H_pre"},
+                     {a->H_post, T * 16, "H_post"},
+                     {a->H_res, T * 64, "H_res"},
+                     {a->grad_x_out, T * 4 * C * 2, "grad_x_out"},
+                     {a->grad_u, T * C * 2, "grad_u"},
+                     {a->grad_x, T * 4 * C * 2, "grad_x"},
+                     {a->grad_f, T * C * 2, "grad_f"},
+                     {a->grad_W, 24 * 4 * C * 4, "grad_W"},
+                     {a->grad_logits, T * 96, "grad_logits"},
+                     {k->x_codes, T * 4 * C, "x_codes"},
+                     {k->x_scales, T * 4 * (C / 32), "x_scales"},
+                     {k->f_codes, T * C, "f_codes"},
+                     {k->f_scales, T * (C / 32), "f_scales"},
+                     {a->workspace, (size_t)need, "workspace"}};
+    s = check_buffers(b, sizeof(b) / sizeof(b[0]));
+    if (s != MHC_OK) return s;
+    return launched(mhc::launch_layer_bwd_ckpt(layer_bwd_ptrs(a, a->workspace),
+                                               mhc::Packed{k->x_codes, k->x_scales},
+                                               mhc::Packed{k->f_codes, k->f_scales}, a->T, a->C,
+                                               k->format, (hipStream_t)stream),
+                    "layer_bwd_ckpt launch");
+}
+
+// ---------------------------------------------------------------------------
+// Microscaled 4-bit quantisation
+// ---------------------------------------------------------------------------
+
+mhc_status mhc_mx4_quantize(const void* x, int32_t dtype, void* codes, uint8_t* scales, int64_t R,
+                            int64_t C, int32_t transpose, void* stream)
+{
+    mhc_status s;
+    if ((s = check_dtype(dtype)) != MHC_OK) return s;
+    if (transpose != 0 && transpose != 1)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "transpose must be 0 or 1, got %d", transpose);
+    if ((s = check_matrix(R, C, transpose ? 8 : 32)) != MHC_OK) return s;
+    if (transpose && R % 32 != 0)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "R must be a multiple of 32 (got %lld)", (long long)R);
+    if (transpose && C > 64 * (int64_t)65535)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "C=%lld out of range", (long long)C);
+    if (R == 0) return ok();
+    const Buf b[] = {{x, (size_t)R * (size_t)C * dtype_bytes(dtype), "x"},
+                     {codes, (size_t)R * (size_t)C / 2, "codes"},
+                     {scales, (size_t)R * (size_t)C / 32, "scales"}};
+    if ((s = check_buffers(b, 3)) != MHC_OK) return s;
+    return launched(mhc::launch_mx4_quantize(x, dtype == MHC_FP32, mhc::Packed{codes, scales}, R, C,
+                                             transpose != 0, (hipStream_t)stream),
+                    "mx4_quantize launch");
+}
+
+mhc_status mhc_mx4_dequantize(const void* codes, const uint8_t* scales, void* x, int32_t dtype,
+                              int64_t R, int64_t C, void* stream)
+{
+    mhc_status s;
+    if ((s = check_dtype(dtype)) != MHC_OK || (s = check_matrix(R, C, 32)) != MHC_OK) return s;
+    if (R == 0) return ok();
+    const Buf b[] = {{codes, (size_t)R * (size_t)C / 2, "codes"},
+                     {scales, (size_t)R * (size_t)C / 32, "scales"},
+                     {x, (size_t)R * (size_t)C * dtype_bytes(dtype), "x"}};
+    if ((s = check_buffers(b, 3)) != MHC_OK) return s;
+    const mhc::Packed in{const_cast<void*>(codes), const_cast<uint8_t*>(scales)};
+    return launched(mhc::launch_mx4_dequantize(in, x, dtype == MHC_FP32, R, C, (hipStream_t)stream),
+                    "mx4_dequantize launch");
 }
 
 const char* mhc_status_string(mhc_status s)

@@ -34,6 +34,7 @@
 
 #include "kernels.h"
 #include "proj4.h"
+#include "qkernels.h"
 #include "wave.h"
 
 namespace mhc {
@@ -888,8 +889,8 @@ LayerPlan layer_plan(int64_t T, int64_t C)
     return p;
 }
 
-hipError_t launch_layer_fwd(const LayerPtrs& a, int64_t T, int64_t C, float eps,
-                            const SolverOpts& o, hipStream_t stream)
+hipError_t launch_layer_maps(const LayerPtrs& a, int64_t T, int64_t C, float eps,
+                             const SolverOpts& o, hipStream_t stream)
 {
     const dim3 g1((unsigned)((T + kMapTok - 1) / kMapTok));
     if (o.solver == 0)
@@ -900,7 +901,29 @@ hipError_t launch_layer_fwd(const LayerPtrs& a, int64_t T, int64_t C, float eps,
         hipLaunchKernelGGL(layer_maps_kernel<1>, g1, dim3(kBlock), 0, stream,
                            (const uint16_t*)a.x, (const uint16_t*)a.W, a.logits, a.rms, a.H_pre,
                            a.H_post, a.H_res, T, C, eps, o);
-    hipError_t e = hipGetLastError();
+    return hipGetLastError();
+}
+
+hipError_t launch_layer_wt(const void* W, void* Wt, int64_t C, hipStream_t stream)
+{
+    hipLaunchKernelGGL(layer_wt_kernel, dim3((unsigned)((4 * C + kBlock - 1) / kBlock)), dim3(kBlock),
+                       0, stream, (const uint16_t*)W, (uint4*)Wt, 4 * C);
+    return hipGetLastError();
+}
+
+hipError_t launch_layer_dw_reduce(const float* partial, float* gW, int64_t C, int64_t groups,
+                                  hipStream_t stream)
+{
+    const int64_t n4 = (int64_t)kMaps * 4 * C / 4;
+    hipLaunchKernelGGL(layer_dw_reduce_kernel, dim3((unsigned)((n4 + kBlock - 1) / kBlock)),
+                       dim3(kBlock), 0, stream, (const float4*)partial, (float4*)gW, n4, groups);
+    return hipGetLastError();
+}
+
+hipError_t launch_layer_fwd(const LayerPtrs& a, int64_t T, int64_t C, float eps,
+                            const SolverOpts& o, hipStream_t stream)
+{
+    const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
     if (e != hipSuccess) return e;
     const dim3 g2((unsigned)((T + kMixTokens - 1) / kMixTokens));
     hipLaunchKernelGGL(layer_mix_kernel, g2, dim3(kBlock), 0, stream, (const uint4*)a.x,
@@ -961,9 +984,7 @@ hipError_t launch_layer_bwd(const LayerPtrs& a, int64_t T, int64_t C, hipStream_
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     uint4* wt = reinterpret_cast<uint4*>(ws + p.off_wt);
-    hipLaunchKernelGGL(layer_wt_kernel, dim3((unsigned)((4 * C + kBlock - 1) / kBlock)), dim3(kBlock),
-                       0, stream, (const uint16_t*)a.W, wt, 4 * C);
-    e = hipGetLastError();
+    e = launch_layer_wt(a.W, wt, C, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(layer_dx_kernel, dim3((unsigned)((T + kDxTok - 1) / kDxTok)), dim3(kBlock), 0,
                        stream, (const uint4*)a.x, (const uint4*)a.grad_x_out, (const uint4*)a.grad_u,
@@ -976,11 +997,7 @@ hipError_t launch_layer_bwd(const LayerPtrs& a, int64_t T, int64_t C, hipStream_
                        dlo, partial, T, p.Tp, C, p.group_tokens);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t n4 = (int64_t)kMaps * 4 * C / 4;
-    hipLaunchKernelGGL(layer_dw_reduce_kernel, dim3((unsigned)((n4 + kBlock - 1) / kBlock)),
-                       dim3(kBlock), 0, stream, (const float4*)partial, (float4*)a.grad_W, n4,
-                       p.groups);
-    return hipGetLastError();
+    return launch_layer_dw_reduce(partial, a.grad_W, C, p.groups, stream);
 }
 
 }  // namespace mhc

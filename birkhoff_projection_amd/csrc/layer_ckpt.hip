@@ -1,0 +1,699 @@
+// The residual-layer step (layer.hip) with x and f kept as 8-bit checkpoints
+// (mxfmt.h) between forward and backward, for gfx950.
+//
+//   mix    read-mix and write-back, and x and f packed in the same pass
+//   dots   per-token reductions from the checkpoints (read only); epilogue:
+//          sigmoid derivative and projection backward -> grad_logits
+//   dx     grad_x, grad_f
+//   dw     grad_W partials on MFMA
+// The maps pass of the forward, the transposition of W and the reduction of
+// the grad_W partials are the plain layer's.
+//
+// The formulas are the plain layer's with xhat, fhat (what the checkpoints
+// stand for) in the place of x, f; the forward's r, logits and maps are those
+// of x itself.  Checkpoints are half the bytes of x in each of the three
+// backward passes that read it.
+//
+// Mixed precision: a checkpoint value is exact in bf16, so MFMA takes it
+// unrounded.  grad_logits / r enters the grad_W product as three bf16 parts,
+// which hold all 24 bits of an fp32 (its sum over the tokens is then as good
+// as in fp32), and the grad_x product as two, enough for a bf16 result.
+#include "mxfmt.h"
+#include "proj4.h"
+#include "qkernels.h"
+#include "wave.h"
+
+namespace mhc {
+
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kMaps = 24;  // n*n + 2n for n = 4
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+MHC_DEV bf16x8 as_bf16x8(const uint4& q) { return __builtin_bit_cast(bf16x8, q); }
+
+// ---------------------------------------------------------------------------
+// mix: read-mix u, write-back x_out and the checkpoints of x and f, 16 tokens
+// per workgroup (spaced by the grid size, so the workgroups stream a
+// contiguous front).
+// ---------------------------------------------------------------------------
+constexpr int kMixTokens = 16;
+
+template <int FMT>
+__global__ __launch_bounds__(kBlock) void layer_mix_ckpt_kernel(
+    const uint4* __restrict__ x, const uint4* __restrict__ f, const float* __restrict__ Hpre,
+    const float* __restrict__ Hpost, const float* __restrict__ Hres, uint4* __restrict__ u,
+    uint4* __restrict__ xo, uint2* __restrict__ xc, uint8_t* __restrict__ xs_out,
+    uint2* __restrict__ fc, uint8_t* __restrict__ fs_out, int64_t T, int64_t C8)
+{
+    __shared__ float sM[kMixTokens][kMaps];
+    const int64_t b = blockIdx.x, G = gridDim.x;
+    const int tid = threadIdx.x;
+    const int64_t per = (T - b + G - 1) / G;
+    const int nt = (int)(per < kMixTokens ? per : kMixTokens);
+    for (int p = tid; p < nt * kMaps; p += kBlock) {
+        const int tl = p / kMaps, m = p % kMaps;
+        const int64_t t = b + G * tl;
+        sM[tl][m] = m < 4 ? Hpre[4 * t + m] : (m < 8 ? Hpost[4 * t + m - 4] : Hres[16 * t + m - 8]);
+    }
+    __syncthreads();
+    for (int tl = 0; tl < nt; ++tl) {
+        float M[kMaps];
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) M[m] = sM[tl][m];
+        const int64_t t = b + G * tl;
+        // C8 is a multiple of 8: a quad of lanes (one block) is whole
+        for (int64_t c = tid; c < C8; c += kBlock) {
+            uint4 xq[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xq[j] = mhc_load_stream(&x[(t * 4 + j) * C8 + c]);
+            const uint4 fq = mhc_load_stream(&f[t * C8 + c]);
+            float xs[4][8], ff[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mx_unpack8(xq[j], xs[j]);
+            mx_unpack8(fq, ff);
+            float uu[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float s = M[0] * xs[0][e];
+                s = __builtin_fmaf(M[1], xs[1][e], s);
+                s = __builtin_fmaf(M[2], xs[2][e], s);
+                uu[e] = __builtin_fmaf(M[3], xs[3][e], s);
+            }
+            mhc_store_stream(&u[t * C8 + c], mx_pack8(uu));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float o8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float s = M[4 + i] * ff[e];
+                    s = __builtin_fmaf(M[8 + 4 * i + 0], xs[0][e], s);
+                    s = __builtin_fmaf(M[8 + 4 * i + 1], xs[1][e], s);
+                    s = __builtin_fmaf(M[8 + 4 * i + 2], xs[2][e], s);
+                    o8[e] = __builtin_fmaf(M[8 + 4 * i + 3], xs[3][e], s);
+                }
+                mhc_store_stream(&xo[(t * 4 + i) * C8 + c], mx_pack8(o8));
+            }
+            const bool lead = (c & 3) == 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t m = mx_quad_max(mx_amax8(xq[j])), s = mx_scale_byte<FMT>(m);
+                mx_store_stream(&xc[(t * 4 + j) * C8 + c], mx_encode8<FMT>(xs[j], m, s));
+                if (lead) xs_out[(t * 4 + j) * (C8 / 4) + (c >> 2)] = (uint8_t)s;
+            }
+            const uint32_t m = mx_quad_max(mx_amax8(fq)), s = mx_scale_byte<FMT>(m);
+            mx_store_stream(&fc[t * C8 + c], mx_encode8<FMT>(ff, m, s));
+            if (lead) fs_out[t * (C8 / 4) + (c >> 2)] = (uint8_t)s;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dots: wave w of workgroup b handles tokens 64 b + 16 w + [0, 16), one token
+// at a time across the wave; lanes stride over the 8-column chunks.  The
+// (token, chunk) steps of a wave form one software pipeline: step i+1's loads
+// are issued into the other register set before step i is consumed (the
+// vector-memory counter retires in order), across token boundaries too.  At
+// a token's last chunk the 24 partial dots are wave-reduced into LDS; then
+// lanes 0..15 each finish one token.
+// ---------------------------------------------------------------------------
+struct DotsLoads {
+    uint2 x[4], f;
+    uint32_t sx[4], sf;
+    uint4 g[4], u;
+};
+
+struct DotsLane {
+    const uint2* xc;
+    const uint8_t* xs;
+    const uint2* fc;
+    const uint8_t* fs;
+    const uint4* gxo;
+    const uint4* gu;
+    int64_t T, C8, nch, tb;
+    int lane;
+};
+
+MHC_DEV void dots_issue(const DotsLane& L, DotsLoads& d, int64_t i)
+{
+    // steps past the wave's last one read clamped addresses and are never consumed
+    int64_t tl = i / L.nch;
+    tl = tl < 16 ? tl : 15;
+    int64_t t = L.tb + tl;
+    t = t < L.T ? t : L.T - 1;
+    int64_t c = L.lane + 64 * (i % L.nch);
+    c = c < L.C8 ? c : L.C8 - 1;
+    const int64_t cb = L.C8 / 4, b = c >> 2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        d.x[j] = L.xc[(t * 4 + j) * L.C8 + c];
+        d.sx[j] = L.xs[(t * 4 + j) * cb + b];
+        d.g[j] = L.gxo[(t * 4 + j) * L.C8 + c];
+    }
+    d.f = L.fc[t * L.C8 + c];
+    d.sf = L.fs[t * cb + b];
+    d.u = L.gu[t * L.C8 + c];
+}
+
+template <int FMT>
+MHC_DEV void dots_consume(const DotsLane& L, const DotsLoads& d, int64_t i, float (&acc)[32],
+                          float (*sDots)[kMaps])
+{
+    const int64_t tl = i / L.nch, ci = i % L.nch;
+    const int64_t t = L.tb + tl;
+    const int64_t c = L.lane + 64 * ci;
+    if (t < L.T && c < L.C8) {
+        float sc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sc[j] = mx_scale(d.sx[j]);
+        const float sf = mx_scale(d.sf);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // 4 columns at a time
+            float xs[4][4], gs[4][4], ff[4], uu[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mx_decode4<FMT>(h ? d.x[j].y : d.x[j].x, sc[j], xs[j]);
+                const uint32_t w0 = h ? d.g[j].z : d.g[j].x, w1 = h ? d.g[j].w : d.g[j].y;
+                gs[j][0] = mhc_bf16_lo(w0);
+                gs[j][1] = mhc_bf16_hi(w0);
+                gs[j][2] = mhc_bf16_lo(w1);
+                gs[j][3] = mhc_bf16_hi(w1);
+            }
+            mx_decode4<FMT>(h ? d.f.y : d.f.x, sf, ff);
+            const uint32_t w0 = h ? d.u.z : d.u.x, w1 = h ? d.u.w : d.u.y;
+            uu[0] = mhc_bf16_lo(w0);
+            uu[1] = mhc_bf16_hi(w0);
+            uu[2] = mhc_bf16_lo(w1);
+            uu[3] = mhc_bf16_hi(w1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] = __builtin_fmaf(uu[e], xs[j][e], acc[j]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[4 + k] = __builtin_fmaf(gs[k][e], ff[e], acc[4 + k]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[8 + 4 * k + j] = __builtin_fmaf(gs[k][e], xs[j][e], acc[8 + 4 * k + j]);
+            }
+        }
+    }
+    if (ci == L.nch - 1) {  // the token's last chunk: reduce its dots
+        const float sm = wave_sum_halving<32>(acc);
+        const int idx = (L.lane >> 1) & 31;
+        if ((L.lane & 1) == 0 && idx < kMaps) sDots[tl][idx] = sm;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+    }
+}
+
+template <int FMT>
+__global__ __launch_bounds__(kBlock) void layer_dots_ckpt_kernel(
+    const uint2* __restrict__ xc, const uint8_t* __restrict__ xs, const uint2* __restrict__ fc,
+    const uint8_t* __restrict__ fs, const uint4* __restrict__ gxo, const uint4* __restrict__ gu,
+    const float* __restrict__ Hpre, const float* __restrict__ Hpost, const float* __restrict__ Hres,
+    const float* __restrict__ logits, const float* __restrict__ rms, float* __restrict__ glogits,
+    float* __restrict__ svec, __bf16* __restrict__ dlT, int64_t T, int64_t Tp, int64_t C8)
+{
+    __shared__ float sDots[4][16][kMaps];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t tb = (int64_t)blockIdx.x * 64 + 16 * w;
+    DotsLane L;
+    L.xc = xc; L.xs = xs; L.fc = fc; L.fs = fs; L.gxo = gxo; L.gu = gu;
+    L.T = T; L.C8 = C8; L.nch = (C8 + 63) / 64; L.tb = tb; L.lane = lane;
+    float acc[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+    // 16 tokens x nch chunks: always an even number of steps
+    const int64_t steps = 16 * L.nch;
+    DotsLoads d0, d1;
+    dots_issue(L, d0, 0);
+    for (int64_t i = 0; i < steps; i += 2) {
+        dots_issue(L, d1, i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        dots_consume<FMT>(L, d0, i, acc, sDots[w]);
+        __builtin_amdgcn_sched_barrier(0);
+        dots_issue(L, d0, i + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        dots_consume<FMT>(L, d1, i + 1, acc, sDots[w]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+    if (lane >= 16) return;
+    const int64_t t = tb + lane;
+    if (t >= Tp) return;
+    float dl[kMaps];
+    if (t < T) {
+        float d[kMaps];
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) d[m] = sDots[w][lane][m];
+        const float4 pq = reinterpret_cast<const float4*>(Hpre)[t];
+        const float4 oq = reinterpret_cast<const float4*>(Hpost)[t];
+        const float hp[4] = {pq.x, pq.y, pq.z, pq.w};
+        const float ho[4] = {oq.x, oq.y, oq.z, oq.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            dl[j] = d[j] * hp[j] * (1.f - hp[j]);
+            dl[4 + j] = d[4 + j] * ho[j] * (1.f - ho[j]);
+        }
+        float H[16];
+        const float4* hr = reinterpret_cast<const float4*>(Hres + 16 * t);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 v = hr[q];
+            H[4 * q] = v.x;
+            H[4 * q + 1] = v.y;
+            H[4 * q + 2] = v.z;
+            H[4 * q + 3] = v.w;
+        }
+        project_bwd(H, d + 8, dl + 8);
+        // RMSNorm coefficient: <dl W, x / r> / (4C) = <dl, logits> / (4C)
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) s = __builtin_fmaf(dl[m], logits[kMaps * t + m], s);
+        svec[t] = s / (float)(32 * C8);
+        float4* go = reinterpret_cast<float4*>(glogits + kMaps * t);
+#pragma unroll
+        for (int q = 0; q < kMaps / 4; ++q) go[q] = make_float4(dl[4 * q], dl[4 * q + 1], dl[4 * q + 2], dl[4 * q + 3]);
+        const float inv = 1.f / rms[t];
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) dl[m] *= inv;
+    } else {
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) dl[m] = 0.f;
+    }
+#pragma unroll
+    for (int m = 0; m < kMaps; ++m) {
+        float v = dl[m];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const __bf16 h = (__bf16)v;
+            dlT[((int64_t)p * kMaps + m) * Tp + t] = h;
+            v -= (float)h;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dx: workgroup = 16 tokens x all columns, in chunks of 128 columns of every
+// stream.  Per chunk wave w forms (dl W)^T of stream w on MFMA (16 k x 16
+// tokens, A from the transposed W, B = dl in two bf16 parts, fixed for the
+// workgroup) into LDS; then an element-wise pass with lane = (token, 8
+// columns) whose accesses cover 4 rows x 256 contiguous bytes.  All loads of
+// chunk i+1 are issued before chunk i is consumed, into the other of two
+// register sets, and the LDS buffer is doubled, so one barrier per chunk
+// suffices.
+// ---------------------------------------------------------------------------
+constexpr int kDxTok = 16;                    // tokens per workgroup (MFMA N)
+constexpr int kDxChunk = 128;                 // columns per stream per chunk
+constexpr int kDxTiles = kDxChunk / 16;       // k-tiles per wave per chunk
+constexpr int kDxPitch = 4 * kDxChunk + 4;    // floats per LDS row (bank spread)
+
+struct DxLoads {
+    uint4 a[kDxTiles];    // transposed-W fragments of this wave's k-tiles
+    uint4 g[4], u;        // grad_x_out, grad_u of the lane's token and columns
+    uint2 x[4];           // checkpoint codes and scales of the same
+    uint32_t sx[4];
+};
+
+struct DxLane {
+    const uint2* xc;
+    const uint8_t* xs;
+    const uint4* gxo;
+    const uint4* gu;
+    const uint4* Wt;
+    uint4* gx;
+    uint4* gf;
+    int64_t C, C8;
+    int64_t tr;      // token row of the element-wise lane (clamped into range)
+    bool tok;        // that token exists
+    int w, row, kq, cl;
+    float H[16], hp[4], ho[4], inv, sr;
+    bf16x8 bhi, blo;
+};
+
+MHC_DEV void dx_issue(const DxLane& L, DxLoads& d, int64_t c0)
+{
+    // Wt rows past C (a ragged last chunk) are clamped; their products land
+    // in LDS columns that the element-wise pass never reads.  Lanes kq = 3
+    // (maps 24..31, which do not exist) load the piece of maps 0..7.
+    const int kqc = L.kq < 3 ? L.kq : 0;
+#pragma unroll
+    for (int s = 0; s < kDxTiles; ++s) {
+        int64_t c = c0 + 16 * s + L.row;
+        c = c < L.C ? c : L.C - 1;
+        d.a[s] = L.Wt[3 * (L.w * L.C + c) + kqc];
+    }
+    const bool col = c0 + 8 * L.cl < L.C;
+    const int64_t c8 = col ? c0 / 8 + L.cl : L.C8 - 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        d.g[i] = L.gxo[(L.tr * 4 + i) * L.C8 + c8];
+        d.x[i] = L.xc[(L.tr * 4 + i) * L.C8 + c8];
+        d.sx[i] = L.xs[(L.tr * 4 + i) * (L.C8 / 4) + (c8 >> 2)];
+    }
+    d.u = L.gu[L.tr * L.C8 + c8];
+}
+
+template <int FMT>
+MHC_DEV void dx_consume(const DxLane& L, const DxLoads& d, float (*sD)[kDxPitch], int64_t c0)
+{
+#pragma unroll
+    for (int s = 0; s < kDxTiles; ++s) {
+        // lanes kq = 3 hold a finite piece of another map range: their B
+        // (maps 24..31) is zero, so they add nothing
+        const bf16x8 a = as_bf16x8(d.a[s]);
+        floatx4 acc = floatx4{0.f, 0.f, 0.f, 0.f};
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, L.bhi, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, L.blo, acc, 0, 0, 0);
+        *reinterpret_cast<floatx4*>(&sD[L.row][L.w * kDxChunk + 16 * s + 4 * L.kq]) = acc;
+    }
+    mhc_lds_barrier();
+    const bool col = c0 + 8 * L.cl < L.C;
+    if (!(L.tok && col)) return;
+    const int tl = 4 * L.w + L.kq;  // element-wise token of this lane
+    const int64_t c8 = c0 / 8 + L.cl;
+    float gs[4][8], uu[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx_unpack8(d.g[i], gs[i]);
+    mx_unpack8(d.u, uu);
+    {
+        float g8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float sm = L.ho[0] * gs[0][e];
+            sm = __builtin_fmaf(L.ho[1], gs[1][e], sm);
+            sm = __builtin_fmaf(L.ho[2], gs[2][e], sm);
+            g8[e] = __builtin_fmaf(L.ho[3], gs[3][e], sm);
+        }
+        mhc_store_stream(&L.gf[L.tr * L.C8 + c8], mx_pack8(g8));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float xs[8], o8[8];
+        mx_decode8<FMT>(d.x[j], mx_scale(d.sx[j]), xs);
+        const floatx4 d0 = *reinterpret_cast<const floatx4*>(&sD[tl][j * kDxChunk + 8 * L.cl]);
+        const floatx4 d1 = *reinterpret_cast<const floatx4*>(&sD[tl][j * kDxChunk + 8 * L.cl + 4]);
+        const float dn[8] = {d0[0], d0[1], d0[2], d0[3], d1[0], d1[1], d1[2], d1[3]};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float sm = L.H[j] * gs[0][e];
+            sm = __builtin_fmaf(L.H[4 + j], gs[1][e], sm);
+            sm = __builtin_fmaf(L.H[8 + j], gs[2][e], sm);
+            sm = __builtin_fmaf(L.H[12 + j], gs[3][e], sm);
+            sm = __builtin_fmaf(L.hp[j], uu[e], sm);
+            o8[e] = __builtin_fmaf(__builtin_fmaf(-xs[e], L.sr, dn[e]), L.inv, sm);
+        }
+        mhc_store_stream(&L.gx[(L.tr * 4 + j) * L.C8 + c8], mx_pack8(o8));
+    }
+}
+
+template <int FMT>
+__global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) void layer_dx_ckpt_kernel(
+    const uint2* __restrict__ xc, const uint8_t* __restrict__ xs, const uint4* __restrict__ gxo,
+    const uint4* __restrict__ gu, const uint4* __restrict__ Wt, const float* __restrict__ Hpre,
+    const float* __restrict__ Hpost, const float* __restrict__ Hres, const float* __restrict__ rms,
+    const float* __restrict__ glogits, const float* __restrict__ svec, uint4* __restrict__ gx,
+    uint4* __restrict__ gf, int64_t T, int64_t C)
+{
+    __shared__ __attribute__((aligned(16))) float sD[2][kDxTok][kDxPitch];
+    DxLane L;
+    const int lane = threadIdx.x & 63;
+    L.xc = xc; L.xs = xs; L.gxo = gxo; L.gu = gu; L.Wt = Wt; L.gx = gx; L.gf = gf;
+    L.C = C; L.C8 = C / 8;
+    L.w = threadIdx.x >> 6;
+    L.row = lane & 15;
+    L.kq = lane >> 4;
+    L.cl = lane & 15;
+    const int64_t t0 = (int64_t)blockIdx.x * kDxTok;
+    // B operand: dl[token t0 + row][maps 8 kq ..+7], two bf16 parts
+    {
+        float b8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b8[e] = 0.f;
+        if (t0 + L.row < T && L.kq < 3) {
+            const float4* src = reinterpret_cast<const float4*>(glogits + kMaps * (t0 + L.row) + 8 * L.kq);
+            const float4 v0 = src[0], v1 = src[1];
+            b8[0] = v0.x; b8[1] = v0.y; b8[2] = v0.z; b8[3] = v0.w;
+            b8[4] = v1.x; b8[5] = v1.y; b8[6] = v1.z; b8[7] = v1.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const __bf16 h = (__bf16)b8[e];
+            L.bhi[e] = h;
+            L.blo[e] = (__bf16)(b8[e] - (float)h);
+        }
+    }
+    {
+        const int64_t t = t0 + 4 * L.w + L.kq;
+        L.tok = t < T;
+        L.tr = L.tok ? t : T - 1;
+        const float4* hr = reinterpret_cast<const float4*>(Hres + 16 * L.tr);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 v = hr[k];
+            L.H[4 * k] = v.x;
+            L.H[4 * k + 1] = v.y;
+            L.H[4 * k + 2] = v.z;
+            L.H[4 * k + 3] = v.w;
+        }
+        const float4 pq = reinterpret_cast<const float4*>(Hpre)[L.tr];
+        L.hp[0] = pq.x; L.hp[1] = pq.y; L.hp[2] = pq.z; L.hp[3] = pq.w;
+        const float4 oq = reinterpret_cast<const float4*>(Hpost)[L.tr];
+        L.ho[0] = oq.x; L.ho[1] = oq.y; L.ho[2] = oq.z; L.ho[3] = oq.w;
+        L.inv = 1.f / rms[L.tr];
+        L.sr = svec[L.tr] * L.inv;
+    }
+    // branch-free pipeline: the chunk count is padded to even, chunks past C
+    // load clamped addresses and do no element-wise work
+    const int64_t n = (C + kDxChunk - 1) / kDxChunk;
+    DxLoads d0, d1;
+    dx_issue(L, d0, 0);
+    for (int64_t ci = 0; ci < n; ci += 2) {
+        dx_issue(L, d1, (ci + 1) * kDxChunk);
+        __builtin_amdgcn_sched_barrier(0);
+        dx_consume<FMT>(L, d0, sD[0], ci * kDxChunk);
+        __builtin_amdgcn_sched_barrier(0);
+        dx_issue(L, d0, (ci + 2) * kDxChunk);
+        __builtin_amdgcn_sched_barrier(0);
+        dx_consume<FMT>(L, d1, sD[1], (ci + 1) * kDxChunk);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dw: workgroup = 128 flattened k x one token group; wave w takes every 4th
+// 32-token chunk of the group:
+//   dW^T tile (32 maps x 16 k) += dlT (32 maps x 32 tokens) * xhat (32 tokens x 16 k)
+// The MFMA B operand wants 8 consecutive tokens of one k per lane, the memory
+// holds 8 consecutive k of one token.  A lane loads 8 k of 8 tokens (16 lanes
+// cover a token's 128 contiguous bytes), decodes them to bf16 and transposes
+// the 8 x 8 square in its own registers, two tokens at a time by byte
+// permutes; MFMA tile nt then holds k = 8 (lane % 16) + nt instead of
+// 16 consecutive k, which only relabels the columns of the result.  So the
+// tile never passes through LDS.  The three bf16 parts of dlT (A, from L2)
+// are issued with the codes, one chunk ahead, into the other of two register
+// sets.  The four waves' partials are summed in LDS and one partial per token
+// group is written, in a fixed order throughout.
+// ---------------------------------------------------------------------------
+constexpr int kDwK = 128;         // flattened k per workgroup
+constexpr int kDwNt = kDwK / 16;  // MFMA tiles
+constexpr int kDwParts = 3;       // bf16 parts of dl / r
+
+struct DwLoads {
+    uint4 a[kDwParts][2];  // dlT parts: maps 16 mt + row, tokens 8 kq ..+7
+    uint2 x[8];            // codes of token 8 kq + e, k 8 row ..+7
+    uint32_t s[8];
+};
+
+MHC_DEV void dw_issue(DwLoads& d, const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
+                      const __bf16* __restrict__ dlT, int64_t tc, int64_t T, int64_t Tp, int64_t D,
+                      int64_t k0, int lane)
+{
+    const int row = lane & 15, kq = lane >> 4;
+    // chunks past the group read a clamped chunk and are not accumulated
+    const int64_t ta = tc + 32 < Tp ? tc : Tp - 32;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+        const int m = 16 * mt + row < kMaps ? 16 * mt + row : kMaps - 1;
+#pragma unroll
+        for (int p = 0; p < kDwParts; ++p)
+            d.a[p][mt] = *reinterpret_cast<const uint4*>(dlT + ((int64_t)p * kMaps + m) * Tp + ta + 8 * kq);
+    }
+    const int64_t k = k0 + 8 * row;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        int64_t t = tc + 8 * kq + e;
+        t = t < T ? t : T - 1;
+        d.x[e] = *reinterpret_cast<const uint2*>(xc + t * D + k);
+        d.s[e] = xs[t * (D / 32) + (k >> 5)];
+    }
+}
+
+template <int FMT>
+MHC_DEV void dw_consume(const DwLoads& d, floatx4 (&acc)[2][kDwNt], bool live)
+{
+    if (!live) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 4 of the lane's 8 columns
+        uint2 v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = mx_decode4_bf16<FMT>(h ? d.x[e].y : d.x[e].x, mx_scale(d.s[e]));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t sel = q & 1 ? 0x07060302u : 0x05040100u;
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[i] = q < 2 ? mx_perm(v[2 * i + 1].x, v[2 * i].x, sel) : mx_perm(v[2 * i + 1].y, v[2 * i].y, sel);
+            const bf16x8 bb = as_bf16x8(make_uint4(b[0], b[1], b[2], b[3]));
+            // A rows 24..31 repeat map 23 (clamped load); they only feed D
+            // rows 24..31, which are never stored.  Smallest parts first.
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int p = kDwParts - 1; p >= 0; --p)
+                    acc[mt][4 * h + q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        as_bf16x8(d.a[p][mt]), bb, acc[mt][4 * h + q], 0, 0, 0);
+        }
+    }
+}
+
+template <int FMT>
+__global__ __launch_bounds__(kBlock) void layer_dw_ckpt_kernel(
+    const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, const __bf16* __restrict__ dlT,
+    float* __restrict__ partial, int64_t T, int64_t Tp, int64_t C, int64_t group_tokens)
+{
+    __shared__ float sR[32][kDwK + 1];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int row = lane & 15, kq = lane >> 4;
+    const int64_t D = 4 * C;
+    const int64_t k0 = (int64_t)blockIdx.x * kDwK;
+    const int64_t g = blockIdx.y;
+    const int64_t tg0 = g * group_tokens;
+    int64_t tg1 = tg0 + group_tokens;
+    if (tg1 > Tp) tg1 = Tp;
+    floatx4 acc[2][kDwNt];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < kDwNt; ++nt) acc[mt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
+    DwLoads d0, d1;
+    const int64_t first = tg0 + 32 * w;
+    dw_issue(d0, xc, xs, dlT, first, T, Tp, D, k0, lane);
+    for (int64_t tc = first; tc < tg1; tc += 256) {
+        dw_issue(d1, xc, xs, dlT, tc + 128, T, Tp, D, k0, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        dw_consume<FMT>(d0, acc, true);
+        __builtin_amdgcn_sched_barrier(0);
+        dw_issue(d0, xc, xs, dlT, tc + 256, T, Tp, D, k0, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        dw_consume<FMT>(d1, acc, tc + 128 < tg1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // sum the four waves' partials: wave 0 writes, the others add in turn
+    for (int ww = 0; ww < 4; ++ww) {
+        if (w == ww) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < kDwNt; ++nt)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        float& dst = sR[16 * mt + 4 * kq + v][8 * row + nt];
+                        dst = (ww == 0 ? 0.f : dst) + acc[mt][nt][v];
+                    }
+        }
+        __syncthreads();
+    }
+    float* out = partial + g * (int64_t)kMaps * D;
+    for (int p = threadIdx.x; p < kMaps * kDwK; p += kBlock) {
+        const int m = p / kDwK, kk = p % kDwK;
+        out[m * D + k0 + kk] = sR[m][kk];
+    }
+}
+
+template <int FMT>
+hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, int64_t T, int64_t C,
+                        hipStream_t stream)
+{
+    const LayerCkptPlan p = layer_ckpt_plan(T, C);
+    char* ws = static_cast<char*>(a.workspace);
+    float* svec = reinterpret_cast<float*>(ws + p.off_s);
+    __bf16* dlT = reinterpret_cast<__bf16*>(ws + p.off_dl);
+    uint4* wt = reinterpret_cast<uint4*>(ws + p.off_wt);
+    float* partial = reinterpret_cast<float*>(ws + p.off_partial);
+    const uint2* xc = static_cast<const uint2*>(x.codes);
+    hipLaunchKernelGGL(layer_dots_ckpt_kernel<FMT>, dim3((unsigned)(p.Tp / 64)), dim3(kBlock), 0,
+                       stream, xc, x.scales, static_cast<const uint2*>(f.codes), f.scales,
+                       (const uint4*)a.grad_x_out, (const uint4*)a.grad_u, a.H_pre, a.H_post,
+                       a.H_res, a.logits, a.rms, a.grad_logits, svec, dlT, T, p.Tp, C / 8);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    e = launch_layer_wt(a.W, wt, C, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(layer_dx_ckpt_kernel<FMT>, dim3((unsigned)((T + kDxTok - 1) / kDxTok)),
+                       dim3(kBlock), 0, stream, xc, x.scales, (const uint4*)a.grad_x_out,
+                       (const uint4*)a.grad_u, wt, a.H_pre, a.H_post, a.H_res, a.rms, a.grad_logits,
+                       svec, (uint4*)a.grad_x, (uint4*)a.grad_f, T, C);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(layer_dw_ckpt_kernel<FMT>, dim3((unsigned)(4 * C / kDwK), (unsigned)p.groups),
+                       dim3(kBlock), 0, stream, (const uint8_t*)x.codes, x.scales, dlT, partial, T,
+                       p.Tp, C, p.group_tokens);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return launch_layer_dw_reduce(partial, a.grad_W, C, p.groups, stream);
+}
+
+template <int FMT>
+hipError_t layer_mix_as(const LayerPtrs& a, const Packed& x, const Packed& f, int64_t T, int64_t C,
+                        hipStream_t stream)
+{
+    hipLaunchKernelGGL(layer_mix_ckpt_kernel<FMT>, dim3((unsigned)((T + kMixTokens - 1) / kMixTokens)),
+                       dim3(kBlock), 0, stream, (const uint4*)a.x, (const uint4*)a.f, a.H_pre,
+                       a.H_post, a.H_res, (uint4*)a.u, (uint4*)a.x_out, (uint2*)x.codes, x.scales,
+                       (uint2*)f.codes, f.scales, T, C / 8);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+LayerCkptPlan layer_ckpt_plan(int64_t T, int64_t C)
+{
+    const LayerPlan base = layer_plan(T, C);
+    LayerCkptPlan p;
+    p.Tp = base.Tp;
+    p.group_tokens = base.group_tokens;
+    p.groups = base.groups;
+    const int64_t D = 4 * C;
+    p.off_s = 0;
+    p.off_dl = (p.Tp * 4 + 255) / 256 * 256;
+    p.off_wt = p.off_dl + (p.Tp * kMaps * 2 * kDwParts + 255) / 256 * 256;
+    p.off_partial = p.off_wt + (D * kMaps * 2 + 255) / 256 * 256;
+    p.bytes = p.off_partial + p.groups * kMaps * D * 4;
+    return p;
+}
+
+hipError_t launch_layer_fwd_ckpt(const LayerPtrs& a, const Packed& x, const Packed& f, int64_t T,
+                                 int64_t C, float eps, int fmt, const SolverOpts& o,
+                                 hipStream_t stream)
+{
+    const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
+    if (e != hipSuccess) return e;
+    return fmt == kE4M3 ? layer_mix_as<kE4M3>(a, x, f, T, C, stream)
+                        : layer_mix_as<kInt8>(a, x, f, T, C, stream);
+}
+
+hipError_t launch_layer_bwd_ckpt(const LayerPtrs& a, const Packed& x, const Packed& f, int64_t T,
+                                 int64_t C, int fmt, hipStream_t stream)
+{
+    return fmt == kE4M3 ? layer_bwd_as<kE4M3>(a, x, f, T, C, stream)
+                        : layer_bwd_as<kInt8>(a, x, f, T, C, stream);
+}
+
+}  // namespace mhc

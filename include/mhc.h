@@ -392,6 +392,106 @@ mhc_status mhc_layer_bwd(const mhc_layer_args* a, void* stream);
 #define MHC_LAYER_NOALLOC_SCRATCH_BYTES ((int64_t)67108864) /* 64 MiB */
 mhc_status mhc_layer_bwd_noalloc(const mhc_layer_args* a, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Activation checkpoints in 8 bits.
+ *
+ * Widening the residual to n streams widens what a training step keeps for
+ * its backward (neo-ai summary, sections on memory and recomputation): x and
+ * f of every layer.  These calls keep them in 8 bits instead of 16, written
+ * by the pass that reads them anyway and read by the backward directly.
+ *
+ * A checkpoint of R rows of C values is
+ *   codes   [R, C] bytes
+ *   scales  [R, ceil(C / 32)] bytes
+ * Each block of 32 consecutive values of a row (the last may be shorter) has
+ * one scale byte s, standing for 2^(s - 127): the smallest power of two with
+ * max|block| <= M * 2^(s - 127), at least `lo` and at most 254.  A code is the
+ * value divided by that, rounded to the nearest element (ties to the even
+ * code):
+ *   MHC_CKPT_E4M3  8-bit floating point, 3 mantissa bits (M = 448, lo = 10):
+ *                  error at most 2^-4 of the value, for values above
+ *                  2^-13 of their block's largest
+ *   MHC_CKPT_INT8  multiples of 1/64 (M = 127/64, lo = 7): error at most
+ *                  1/127 of the block's largest value
+ * `lo` keeps every stored value zero or a normal bf16 number, and a finite
+ * value never becomes an infinity (an element that would stand for 2^128 is
+ * not used: the largest one below it is).  A block that holds an infinity or
+ * a NaN has s = 255 and reads back as NaN. */
+typedef enum { MHC_CKPT_E4M3 = 0, MHC_CKPT_INT8 = 1 } mhc_ckpt_format;
+typedef enum { MHC_BF16 = 0, MHC_FP32 = 1 } mhc_dtype;
+
+/* mhc_ckpt_pack / mhc_ckpt_unpack -- rows to a checkpoint and back (unpack is
+ * exact in both types).
+ *   x       [R, C] bf16 or fp32 (dtype), device
+ *   codes, scales   as above, device
+ *   R >= 0, C a positive multiple of 8; no output may overlap another tensor */
+mhc_status mhc_ckpt_pack(const void* x, int32_t dtype, void* codes, uint8_t* scales, int64_t R,
+                         int64_t C, int32_t format, void* stream);
+mhc_status mhc_ckpt_unpack(const void* codes, const uint8_t* scales, void* x, int32_t dtype,
+                           int64_t R, int64_t C, int32_t format, void* stream);
+
+/* mhc_stream_mix_ckpt -- mhc_stream_mix that also writes the checkpoint of x
+ * (codes [T,4,C], scales [T,4,ceil(C/32)]) in the same pass.  out and H_out
+ * are mhc_stream_mix's, bit for bit.  No output may overlap another tensor,
+ * except that H_out may be the logits exactly. */
+mhc_status mhc_stream_mix_ckpt(const void* x, const float* H_or_logits, float* H_out, void* out,
+                               void* codes, uint8_t* scales, int64_t T, int32_t n, int64_t C,
+                               int32_t format, const mhc_proj_opts* proj, void* stream);
+
+/* mhc_stream_mix_bwd_ckpt -- mhc_stream_mix_bwd with x read from its
+ * checkpoint (xhat, what the checkpoint stands for, in the place of x):
+ * grad_x does not depend on x and is mhc_stream_mix_bwd's; grad_H[t,i,j] =
+ * sum_c grad_out[t,i,c] xhat[t,j,c]. */
+mhc_status mhc_stream_mix_bwd_ckpt(const void* codes, const uint8_t* scales, const float* H,
+                                   const void* grad_out, void* grad_x, float* grad_H, int64_t T,
+                                   int32_t n, int64_t C, int32_t format, void* stream);
+
+/* Checkpoints of one layer step's x and f (device). */
+typedef struct {
+    int32_t format;     /* mhc_ckpt_format */
+    void* x_codes;      /* [T, 4, C] bytes */
+    uint8_t* x_scales;  /* [T, 4, C/32] */
+    void* f_codes;      /* [T, C] bytes */
+    uint8_t* f_scales;  /* [T, C/32] */
+} mhc_layer_ckpt;
+
+/* mhc_layer_fwd_ckpt -- mhc_layer_fwd that also writes the checkpoints of x
+ * and f, in the pass that reads both; its other outputs are mhc_layer_fwd's,
+ * bit for bit.  No output may overlap another tensor. */
+mhc_status mhc_layer_fwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* ckpt, void* stream);
+
+/* mhc_layer_bwd_ckpt -- mhc_layer_bwd from the checkpoints: xhat and fhat in
+ * the place of x and f (a->x and a->f are ignored), with the forward's rms,
+ * logits and maps, which were computed from x itself.  The workspace is at
+ * least mhc_layer_ckpt_workspace_bytes() bytes, 256-byte aligned, and must
+ * not be in use by another call that overlaps on the device. */
+int64_t mhc_layer_ckpt_workspace_bytes(int64_t T, int32_t n, int64_t C);
+mhc_status mhc_layer_bwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* ckpt, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MXFP4): quantisation and products, for
+ * the linear maps of the layer function between read-mix and write-back.
+ *
+ * A quantised matrix of R rows of C values is
+ *   codes   [R, C/2] bytes, two values a byte, the even one in the low half;
+ *           a value is sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales  [R, C/32] bytes, s standing for 2^(s - 127), 255 for NaN
+ * Quantisation takes the scale of a block of 32 as for the checkpoints, with
+ * M = 6 and lo = 2, and rounds to the nearest value, ties to the even code.
+ * Any scale byte is accepted where a quantised matrix is read. */
+
+/* mhc_mx4_quantize -- x [R, C] bf16 or fp32 to MXFP4.
+ *   transpose = 0: blocks along the rows; codes [R, C/2], scales [R, C/32];
+ *                  C a positive multiple of 32
+ *   transpose = 1: the quantised transpose, blocks along the columns; codes
+ *                  [C, R/2], scales [C, R/32]; R a multiple of 32, C of 8
+ * mhc_mx4_dequantize -- back to bf16 or fp32 rows (exact in fp32; in bf16 for
+ * scale bytes of at least 2). */
+mhc_status mhc_mx4_quantize(const void* x, int32_t dtype, void* codes, uint8_t* scales, int64_t R,
+                            int64_t C, int32_t transpose, void* stream);
+mhc_status mhc_mx4_dequantize(const void* codes, const uint8_t* scales, void* x, int32_t dtype,
+                              int64_t R, int64_t C, void* stream);
+
 const char* mhc_status_string(mhc_status s);
 /* Message for the calling thread's last non-OK status ("" if none). */
 const char* mhc_last_error(void);
