@@ -12,15 +12,17 @@ from .ops import (BirkhoffProjection, birkhoff_bwd, birkhoff_bwd_n, birkhoff_bwd
                   birkhoff_project,
                   layer_bwd, layer_bwd_noalloc, layer_fwd, layer_workspace, make_opts,
                   stream_mix, stream_mix_bwd)
-from .packed import (ProjectedMix, ckpt_pack, ckpt_unpack, layer_bwd_ckpt, layer_ckpt_workspace,
-                     layer_fwd_ckpt, mx4_dequantize, mx4_quantize, projected_mix,
-                     stream_mix_bwd_ckpt, stream_mix_ckpt)
+from .packed import (Mx4Linear, ProjectedMix, ckpt_pack, ckpt_unpack, layer_bwd_ckpt,
+                     layer_ckpt_workspace, layer_fwd_ckpt, layer_read, mx4_dequantize, mx4_linear,
+                     mx4_matmul, mx4_quantize, mx4_write_back, projected_mix, stream_mix_bwd_ckpt,
+                     stream_mix_ckpt)
 
 __all__ = ["LIB_PATH", "MHCError", "lib", "BirkhoffProjection", "birkhoff_bwd",
            "birkhoff_bwd_n", "birkhoff_bwd_recompute", "birkhoff_fwd_bwd", "birkhoff_fwd_n",
            "birkhoff_fwd", "birkhoff_pipeline_step", "birkhoff_project", "layer_bwd", "layer_bwd_noalloc", "layer_fwd",
            "layer_workspace",
            "make_opts", "stream_mix", "stream_mix_bwd",
-           "ProjectedMix", "ckpt_pack", "ckpt_unpack", "layer_bwd_ckpt", "layer_ckpt_workspace",
-           "layer_fwd_ckpt", "mx4_dequantize", "mx4_quantize", "projected_mix",
-           "stream_mix_bwd_ckpt", "stream_mix_ckpt"]
+           "Mx4Linear", "ProjectedMix", "ckpt_pack", "ckpt_unpack", "layer_bwd_ckpt",
+           "layer_ckpt_workspace", "layer_fwd_ckpt", "layer_read", "mx4_dequantize", "mx4_linear",
+           "mx4_matmul", "mx4_quantize", "mx4_write_back", "projected_mix", "stream_mix_bwd_ckpt",
+           "stream_mix_ckpt"]

@@ -83,6 +83,16 @@ SIGNATURES = {
                                    c_int32, c_void_p]),
     "mhc_mx4_dequantize": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64,
                                      c_void_p]),
+    "mhc_mx4_matmul": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64,
+                                 c_int64, c_int64, c_void_p]),
+    "mhc_mx4_matmul_values_workspace_bytes": (c_int64, [c_int64, c_int64, c_int64]),
+    "mhc_mx4_matmul_values": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                        c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p]),
+    "mhc_mx4_write_back": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_int64,
+                                     c_int64, c_void_p]),
+    "mhc_layer_read_workspace_bytes": (c_int64, [c_int64, c_int32, c_int64]),
+    "mhc_layer_read": (c_int32, [ctypes.POINTER(LayerArgs), c_void_p, c_void_p, c_void_p]),
     "mhc_status_string": (ctypes.c_char_p, [c_int32]),
     "mhc_last_error": (ctypes.c_char_p, []),
     "mhc_abi_version": (c_int32, []),

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmhc.so")
 SOURCES = ["abi.hip", "birkhoff.hip", "birkhoffn.hip", "mix.hip", "layer.hip", "ckpt.hip",
-           "layer_ckpt.hip"]
+           "layer_ckpt.hip", "read.hip", "mx4.hip"]
 ARCH = "gfx950"
 
 

@@ -525,6 +525,26 @@ mhc_status check_matrix(int64_t R, int64_t C, int64_t step)
     return MHC_OK;
 }
 
+// As check_buffers, for calls whose inputs may share memory (a matrix times
+// its own transpose): bit i of `outputs` marks buffer i as written, and only
+// those must be apart from every other buffer.
+mhc_status check_inputs_and_outputs(const Buf* b, int nb, unsigned outputs)
+{
+    for (int i = 0; i < nb; ++i) {
+        if (b[i].p == nullptr) return fail(MHC_ERR_INVALID_ARGUMENT, "%s must not be NULL", b[i].name);
+        if (!aligned16(b[i].p)) return fail(MHC_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", b[i].name);
+    }
+    for (int i = 0; i < nb; ++i)
+        for (int j = i + 1; j < nb; ++j)
+            if ((((outputs >> i) | (outputs >> j)) & 1u) && overlap(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
+                return fail(MHC_ERR_INVALID_ARGUMENT, "%s overlaps %s", b[i].name, b[j].name);
+    return MHC_OK;
+}
+
+// A packed matrix in one workspace: codes, then scales from a multiple of 256.
+int64_t mx4_scales_at(int64_t M, int64_t K) { return (M * (K / 2) + 255) / 256 * 256; }
+int64_t mx4_packed_bytes(int64_t M, int64_t K) { return mx4_scales_at(M, K) + M * (K / 32); }
+
 size_t dtype_bytes(int32_t dtype) { return dtype == MHC_FP32 ? 4 : 2; }
 
 mhc_status check_mix_shape(int64_t T, int32_t n, int64_t C)
@@ -739,6 +759,144 @@ mhc_status mhc_mx4_dequantize(const void* codes, const uint8_t* scales, void* x,
     const mhc::Packed in{const_cast<void*>(codes), const_cast<uint8_t*>(scales)};
     return launched(mhc::launch_mx4_dequantize(in, x, dtype == MHC_FP32, R, C, (hipStream_t)stream),
                     "mx4_dequantize launch");
+}
+
+// ---------------------------------------------------------------------------
+// Microscaled 4-bit products, and the read half of the layer
+// ---------------------------------------------------------------------------
+
+// M x K times (N x K)^T: sizes whose grids and 32-bit tile counts hold
+static mhc_status check_product(int64_t M, int64_t N, int64_t K)
+{
+    if (K < 32 || K % 32 != 0 || K > ((int64_t)1 << 24))
+        return fail(MHC_ERR_INVALID_ARGUMENT, "K must be a positive multiple of 32 (got %lld)", (long long)K);
+    if (N < 8 || N % 8 != 0 || N > ((int64_t)1 << 24))
+        return fail(MHC_ERR_INVALID_ARGUMENT, "N must be a positive multiple of 8 (got %lld)", (long long)N);
+    if (M < 0 || M > kMaxTokens || ((M + 255) / 256) * ((N + 255) / 256) > ((int64_t)1 << 23))
+        return fail(MHC_ERR_INVALID_ARGUMENT, "M=%lld out of range for N=%lld", (long long)M, (long long)N);
+    return MHC_OK;
+}
+
+mhc_status mhc_mx4_matmul(const void* a_codes, const uint8_t* a_scales, const void* b_codes,
+                          const uint8_t* b_scales, void* out, int32_t out_dtype, int64_t M,
+                          int64_t N, int64_t K, void* stream)
+{
+    mhc_status s;
+    if ((s = check_dtype(out_dtype)) != MHC_OK || (s = check_product(M, N, K)) != MHC_OK) return s;
+    if (M == 0) return ok();
+    const Buf b[] = {{a_codes, (size_t)(M * (K / 2)), "a_codes"}, {a_scales, (size_t)(M * (K / 32)), "a_scales"},
+                     {out, (size_t)(M * N) * dtype_bytes(out_dtype), "out"},
+                     {b_codes, (size_t)(N * (K / 2)), "b_codes"}, {b_scales, (size_t)(N * (K / 32)), "b_scales"}};
+    if ((s = check_inputs_and_outputs(b, 5, 1u << 2)) != MHC_OK) return s;
+    const mhc::Packed pa{const_cast<void*>(a_codes), const_cast<uint8_t*>(a_scales)};
+    const mhc::Packed pb{const_cast<void*>(b_codes), const_cast<uint8_t*>(b_scales)};
+    return launched(mhc::launch_mx4_matmul(pa, pb, out, out_dtype == MHC_FP32, M, N, K, (hipStream_t)stream),
+                    "mx4_matmul launch");
+}
+
+int64_t mhc_mx4_matmul_values_workspace_bytes(int64_t M, int64_t N, int64_t K)
+{
+    if (check_product(M, N, K) != MHC_OK) return -1;
+    return mhc::mx4_fuses_quantize(M, K) ? 0 : mx4_packed_bytes(M, K);
+}
+
+mhc_status mhc_mx4_matmul_values(const void* a, int32_t a_dtype, const void* b_codes,
+                                 const uint8_t* b_scales, void* out, int32_t out_dtype, int64_t M,
+                                 int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                                 void* stream)
+{
+    mhc_status s;
+    if ((s = check_dtype(a_dtype)) != MHC_OK || (s = check_dtype(out_dtype)) != MHC_OK ||
+        (s = check_product(M, N, K)) != MHC_OK)
+        return s;
+    if (M == 0) return ok();
+    const int64_t need = mhc_mx4_matmul_values_workspace_bytes(M, N, K);
+    const Buf b[] = {{a, (size_t)(M * K) * dtype_bytes(a_dtype), "a"},
+                     {b_codes, (size_t)(N * (K / 2)), "b_codes"}, {b_scales, (size_t)(N * (K / 32)), "b_scales"},
+                     {out, (size_t)(M * N) * dtype_bytes(out_dtype), "out"},
+                     {workspace, (size_t)need, "workspace"}};
+    if ((s = check_inputs_and_outputs(b, need > 0 ? 5 : 4, (1u << 3) | (1u << 4))) != MHC_OK) return s;
+    const mhc::Packed pb{const_cast<void*>(b_codes), const_cast<uint8_t*>(b_scales)};
+    if (need == 0)
+        return launched(mhc::launch_mx4_matmul_fused(a, a_dtype == MHC_FP32, pb, out, out_dtype == MHC_FP32,
+                                                     M, N, K, (hipStream_t)stream),
+                        "mx4_matmul_values launch");
+    if (workspace_bytes < need)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "workspace_bytes=%lld < %lld required",
+                    (long long)workspace_bytes, (long long)need);
+    const mhc::Packed pa{workspace, static_cast<uint8_t*>(workspace) + mx4_scales_at(M, K)};
+    if ((s = launched(mhc::launch_mx4_quantize(a, a_dtype == MHC_FP32, pa, M, K, false, (hipStream_t)stream),
+                      "mx4_matmul_values: quantise launch")) != MHC_OK)
+        return s;
+    return launched(mhc::launch_mx4_matmul(pa, pb, out, out_dtype == MHC_FP32, M, N, K, (hipStream_t)stream),
+                    "mx4_matmul_values launch");
+}
+
+mhc_status mhc_mx4_write_back(const void* a_codes, const uint8_t* a_scales, const void* b_codes,
+                              const uint8_t* b_scales, const void* x, const float* H_post,
+                              const float* H_res, void* x_out, void* f_out, int64_t T, int32_t n,
+                              int64_t C, int64_t K, void* stream)
+{
+    mhc_status s;
+    if ((s = check_mix_shape(T, n, C)) != MHC_OK || (s = check_product(T, C, K)) != MHC_OK) return s;
+    if (T == 0) return ok();
+    const Buf b[] = {{a_codes, (size_t)(T * (K / 2)), "a_codes"}, {a_scales, (size_t)(T * (K / 32)), "a_scales"},
+                     {b_codes, (size_t)(C * (K / 2)), "b_codes"}, {b_scales, (size_t)(C * (K / 32)), "b_scales"},
+                     {x, (size_t)T * 4 * (size_t)C * 2, "x"}, {H_post, (size_t)T * 16, "H_post"},
+                     {H_res, (size_t)T * 64, "H_res"}, {x_out, (size_t)T * 4 * (size_t)C * 2, "x_out"},
+                     {f_out, (size_t)T * (size_t)C * 2, "f_out"}};
+    if ((s = check_inputs_and_outputs(b, f_out != nullptr ? 9 : 8, (1u << 7) | (1u << 8))) != MHC_OK) return s;
+    const mhc::Packed pa{const_cast<void*>(a_codes), const_cast<uint8_t*>(a_scales)};
+    const mhc::Packed pb{const_cast<void*>(b_codes), const_cast<uint8_t*>(b_scales)};
+    return launched(mhc::launch_mx4_write_back(pa, pb, x, H_post, H_res, x_out, f_out, T, C, K,
+                                               (hipStream_t)stream),
+                    "mx4_write_back launch");
+}
+
+int64_t mhc_layer_read_workspace_bytes(int64_t T, int32_t n, int64_t C)
+{
+    if (check_layer_shape(T, n, C) != MHC_OK) return -1;
+    return mhc::read_plan(T, C).bytes;
+}
+
+mhc_status mhc_layer_read(const mhc_layer_args* a, void* u_codes, uint8_t* u_scales, void* stream)
+{
+    if (a == nullptr) return fail(MHC_ERR_INVALID_ARGUMENT, "args is NULL");
+    mhc_status s = check_layer_shape(a->T, a->n, a->C);
+    if (s != MHC_OK) return s;
+    if (!(a->eps > 0.f) || !(a->eps < 1.f)) return fail(MHC_ERR_INVALID_ARGUMENT, "eps must be in (0, 1)");
+    mhc::SolverOpts o;
+    s = check_opts(a->proj, &o);
+    if (s != MHC_OK) return s;
+    if ((u_codes == nullptr) != (u_scales == nullptr))
+        return fail(MHC_ERR_INVALID_ARGUMENT, "u_codes and u_scales must be given together");
+    if (a->T == 0) return ok();
+    if (a->u == nullptr && u_codes == nullptr)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "u or u_codes must be given");
+    const size_t T = (size_t)a->T, C = (size_t)a->C;
+    const int64_t need = mhc::read_plan(a->T, a->C).bytes;
+    if (need > 0 && a->workspace_bytes < need)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "workspace_bytes=%lld < %lld required",
+                    (long long)a->workspace_bytes, (long long)need);
+    Buf b[12] = {{a->x, T * 4 * C * 2, "x"},       {a->W, 24 * 4 * C * 2, "W"},
+                 {a->rms, T * 4, "rms"},           {a->logits, T * 96, "logits"},
+                 {a->H_pre, T * 16, "H_pre"},      {a->H_post, T * 16, "H_post"},
+                 {a->H_res, T * 64, "H_res"}};
+    int nb = 7;
+    if (a->u != nullptr) b[nb++] = {a->u, T * C * 2, "u"};
+    if (u_codes != nullptr) {
+        b[nb++] = {u_codes, T * C / 2, "u_codes"};
+        b[nb++] = {u_scales, T * C / 32, "u_scales"};
+    }
+    if (need > 0) b[nb++] = {a->workspace, (size_t)need, "workspace"};
+    s = check_buffers(b, nb);
+    if (s != MHC_OK) return s;
+    const mhc::LayerPtrs p{a->x,   a->W,      nullptr,   a->u,     nullptr, a->rms,
+                           a->logits, a->H_pre, a->H_post, a->H_res, nullptr, nullptr,
+                           nullptr, nullptr,  nullptr,  nullptr,  a->workspace};
+    return launched(mhc::launch_layer_read(p, mhc::Packed{u_codes, u_scales}, a->T, a->C, a->eps, o,
+                                           (hipStream_t)stream),
+                    "layer_read launch");
 }
 
 const char* mhc_status_string(mhc_status s)

@@ -31,6 +31,19 @@ hipError_t launch_mx4_quantize(const void* x, bool f32, const Packed& out, int64
                                bool transpose, hipStream_t stream);
 hipError_t launch_mx4_dequantize(const Packed& in, void* x, bool f32, int64_t R, int64_t C,
                                  hipStream_t stream);
+// y [M,N] = a b^T for MXFP4 a [M,K], b [N,K]; f32: y is fp32 instead of bf16.
+hipError_t launch_mx4_matmul(const Packed& a, const Packed& b, void* out, bool f32, int64_t M,
+                             int64_t N, int64_t K, hipStream_t stream);
+// The same with a given as bf16 or fp32 values and quantised in the product's
+// own kernel, for the shapes that mx4_fuses_quantize admits (few rows).
+bool mx4_fuses_quantize(int64_t M, int64_t K);
+hipError_t launch_mx4_matmul_fused(const void* a, bool a_f32, const Packed& b, void* out, bool f32,
+                                   int64_t M, int64_t N, int64_t K, hipStream_t stream);
+// x_out [T,4,C] = H_post (x) (a b^T) + H_res x, and a b^T itself to f_out if
+// that is not NULL.
+hipError_t launch_mx4_write_back(const Packed& a, const Packed& b, const void* x,
+                                 const float* Hpost, const float* Hres, void* x_out, void* f_out,
+                                 int64_t T, int64_t C, int64_t K, hipStream_t stream);
 
 // Parts of the plain layer step (layer.hip) that the checkpointed one shares:
 // the maps pass of the forward, the transposition of W to [4C][24] bf16, and
@@ -40,6 +53,16 @@ hipError_t launch_layer_maps(const LayerPtrs& a, int64_t T, int64_t C, float eps
 hipError_t launch_layer_wt(const void* W, void* Wt, int64_t C, hipStream_t stream);
 hipError_t launch_layer_dw_reduce(const float* partial, float* gW, int64_t C, int64_t groups,
                                   hipStream_t stream);
+
+// The read half of the layer step: a.rms .. a.H_res, and u as bf16 (a.u) and /
+// or MXFP4 (u4), each if its pointer is not NULL.  a.workspace holds
+// read_plan().bytes bytes (fp32 partials [splits][T][25]; none for many tokens).
+struct ReadPlan {
+    int64_t splits, steps_per, bytes;
+};
+ReadPlan read_plan(int64_t T, int64_t C);
+hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, int64_t C, float eps,
+                             const SolverOpts& o, hipStream_t stream);
 
 // Backward workspace: s[Tp] fp32 | dl^T / r in three bf16 parts [3][24][Tp] |
 // W^T [4C][24] bf16 | grad_W partials [groups][24][4C] fp32 (each 256-byte

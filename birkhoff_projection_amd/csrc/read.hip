@@ -1,0 +1,262 @@
+// The read half of the residual-layer step (layer.hip) on its own, for gfx950:
+// the token's maps and the layer function's input u = sum_j H_pre[j] x_j, as
+// bf16 or quantised to MXFP4 (mxfmt.h) in the same pass.
+//
+// Many tokens: the layer's maps pass, then one pass over x for u.
+//
+// Few tokens: that maps pass runs one workgroup per 64 tokens, each walking
+// the whole width 4C, so a single token would take as long as 16384.  Here
+// the width is split over the grid instead:
+//   part    16 tokens x one piece of the width per workgroup: MFMA partial
+//           logits and sums of squares, written as partials [S][T][25]
+//   finish  one workgroup per token: the partials summed in a fixed order,
+//           maps and projection, then u (the projection runs in one wave
+//           while the others go on to u, which does not need it)
+#include "mxfmt.h"
+#include "proj4.h"
+#include "qkernels.h"
+#include "wave.h"
+
+namespace mhc {
+
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kMaps = 24;
+constexpr int kVals = kMaps + 1;  // logits and the sum of squares
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+MHC_DEV float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+// u of 8 columns, stored as bf16 and / or MXFP4.  The 4-bit codes are those of
+// the bf16 u, so they do not depend on whether u itself is kept.  Quads of
+// lanes must be whole.
+struct UOut {
+    uint4* u;          // [T, C] bf16 or NULL
+    uint32_t* codes;   // [T, C/2] or NULL
+    uint8_t* scales;   // [T, C/32]
+};
+
+MHC_DEV void store_u(const UOut& o, int64_t i, const float (&M)[4], const uint4 (&xq)[4])
+{
+    float xs[4][8], uu[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mx_unpack8(xq[j], xs[j]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float s = M[0] * xs[0][e];
+        s = __builtin_fmaf(M[1], xs[1][e], s);
+        s = __builtin_fmaf(M[2], xs[2][e], s);
+        uu[e] = __builtin_fmaf(M[3], xs[3][e], s);
+    }
+    const uint4 q = mx_pack8(uu);
+    if (o.u != nullptr) mhc_store_stream(&o.u[i], q);
+    if (o.codes != nullptr) {
+        const uint32_t amax = mx_quad_max(mx_amax8(q)), s = mx_scale_byte<kE2M1>(amax);
+        o.codes[i] = mx_encode8_e2m1(q, amax, s);
+        if ((i & 3) == 0) o.scales[i >> 2] = (uint8_t)s;
+    }
+}
+
+// u for many tokens: 16 tokens per workgroup, spaced by the grid size.
+constexpr int kMixTokens = 16;
+
+__global__ __launch_bounds__(kBlock) void read_mix_kernel(const uint4* __restrict__ x,
+                                                          const float* __restrict__ Hpre, UOut o,
+                                                          int64_t T, int64_t C8)
+{
+    const int64_t b = blockIdx.x, G = gridDim.x;
+    const int tid = threadIdx.x;
+    for (int tl = 0; tl < kMixTokens; ++tl) {
+        const int64_t t = b + G * tl;
+        if (t >= T) return;
+        const float4 h = reinterpret_cast<const float4*>(Hpre)[t];
+        const float M[4] = {h.x, h.y, h.z, h.w};
+        // C8 is a multiple of 8: a quad of lanes (one block) is whole
+        for (int64_t c = tid; c < C8; c += kBlock) {
+            uint4 xq[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xq[j] = mhc_load_stream(&x[(t * 4 + j) * C8 + c]);
+            store_u(o, t * C8 + c, M, xq);
+        }
+    }
+}
+
+// Partial logits: 4 waves take the 32-wide steps of the workgroup's piece of
+// the width in turn.  MFMA 16x16x32: A = x rows (token l % 16, k 8 (l / 16)),
+// B = W rows (map l % 16), D lane l, v: token 4 (l / 16) + v, map l % 16.
+constexpr int kPartTok = 16;
+
+__global__ __launch_bounds__(kBlock) void read_part_kernel(const uint16_t* __restrict__ x,
+                                                           const uint16_t* __restrict__ W,
+                                                           float* __restrict__ partial, int64_t T,
+                                                           int64_t D, int64_t steps_per)
+{
+    __shared__ float sR[4][kPartTok][32];
+    __shared__ float sQ[4][kPartTok];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int row = lane & 15, kq = lane >> 4;
+    const int64_t t0 = (int64_t)blockIdx.x * kPartTok;
+    int64_t t = t0 + row;
+    t = t < T ? t : T - 1;
+    const uint16_t* xp = x + t * D + 8 * kq;
+    const uint16_t* w0 = W + row * D + 8 * kq;
+    const uint16_t* w1 = W + (16 + (row & 7)) * D + 8 * kq;  // maps 16..23, twice
+    const int64_t s0 = (int64_t)blockIdx.y * steps_per;
+    int64_t s1 = s0 + steps_per;
+    s1 = s1 < D / 32 ? s1 : D / 32;
+    floatx4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = acc0;
+    float ssq = 0.f;
+    for (int64_t s = s0 + w; s < s1; s += 16) {  // 4 steps' loads at once
+        uint4 a[4], b0[4], b1[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t at = s + 4 * i < s1 ? s + 4 * i : s;
+            a[i] = *reinterpret_cast<const uint4*>(xp + 32 * at);
+            b0[i] = *reinterpret_cast<const uint4*>(w0 + 32 * at);
+            b1[i] = *reinterpret_cast<const uint4*>(w1 + 32 * at);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (s + 4 * i >= s1) break;
+            acc0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, a[i]), __builtin_bit_cast(bf16x8, b0[i]), acc0, 0, 0, 0);
+            acc1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, a[i]), __builtin_bit_cast(bf16x8, b1[i]), acc1, 0, 0, 0);
+            float f[8];
+            mx_unpack8(a[i], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ssq = __builtin_fmaf(f[e], f[e], ssq);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        sR[w][4 * kq + v][row] = acc0[v];
+        if (row < 8) sR[w][4 * kq + v][16 + row] = acc1[v];
+    }
+    ssq = sum_bit5(sum_bit4(ssq));
+    if (kq == 0) sQ[w][row] = ssq;
+    __syncthreads();
+    for (int p = threadIdx.x; p < kPartTok * kVals; p += kBlock) {
+        const int tl = p / kVals, m = p % kVals;
+        if (t0 + tl >= T) break;
+        const float v = m < kMaps ? (sR[0][tl][m] + sR[1][tl][m]) + (sR[2][tl][m] + sR[3][tl][m])
+                                  : (sQ[0][tl] + sQ[1][tl]) + (sQ[2][tl] + sQ[3][tl]);
+        partial[((int64_t)blockIdx.y * T + t0 + tl) * kVals + m] = v;
+    }
+}
+
+template <int SOLVER>
+__global__ __launch_bounds__(kBlock) void read_finish_kernel(
+    const uint4* __restrict__ x, const float* __restrict__ partial, int splits,
+    float* __restrict__ logits, float* __restrict__ rms, float* __restrict__ Hpre,
+    float* __restrict__ Hpost, float* __restrict__ Hres, UOut o, int64_t T, int64_t C8, float eps,
+    SolverOpts opts)
+{
+    __shared__ float sP[8][32];
+    __shared__ float sL[kVals];
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x;
+    {
+        const int m = tid & 31, g = tid >> 5;
+        float s = 0.f;
+        if (m < kVals)
+            for (int k = g; k < splits; k += 8) s += partial[((int64_t)k * T + t) * kVals + m];
+        sP[g][m] = s;
+    }
+    __syncthreads();
+    if (tid < kVals) {
+        float s = 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) s += sP[g][tid];
+        sL[tid] = s;
+    }
+    __syncthreads();
+    const float r = sqrtf(sL[kMaps] / (float)(32 * C8) + eps);
+    const float inv = 1.f / r;
+    if (tid < kMaps) {
+        const float l = sL[tid] * inv;
+        logits[kMaps * t + tid] = l;
+        if (tid == 0) rms[t] = r;
+        if (tid < 4) Hpre[4 * t + tid] = sigmoid(l);
+        else if (tid < 8) Hpost[4 * t + tid - 4] = sigmoid(l);
+    }
+    if (tid < 64) {  // wave 0: the projection (one lane), the others go on to u
+        if (tid == 0) {
+            float a[16], h[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) a[k] = sL[8 + k] * inv;
+            if (SOLVER == 0)
+                project_newton(a, h, opts);
+            else
+                project_sinkhorn(a, h, opts);
+            float4* ho = reinterpret_cast<float4*>(Hres + 16 * t);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ho[q] = make_float4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+        }
+        return;
+    }
+    float M[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) M[j] = sigmoid(sL[j] * inv);
+    for (int64_t c = tid - 64; c < C8; c += kBlock - 64) {
+        uint4 xq[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xq[j] = x[(t * 4 + j) * C8 + c];
+        store_u(o, t * C8 + c, M, xq);
+    }
+}
+
+}  // namespace
+
+// Up to kReadFewTokens tokens take the split kernels, with about 512
+// workgroups in all and at least 16 steps of 32 (4 per wave) each.
+constexpr int64_t kReadFewTokens = 2048;
+
+ReadPlan read_plan(int64_t T, int64_t C)
+{
+    ReadPlan p{0, 0, 0};
+    if (T > kReadFewTokens) return p;
+    const int64_t steps = 4 * C / 32, tiles = (T + kPartTok - 1) / kPartTok;
+    int64_t want = (512 + tiles - 1) / tiles;
+    if (want > steps / 16) want = steps / 16;
+    if (want < 1) want = 1;
+    p.steps_per = (steps + want - 1) / want;
+    p.splits = (steps + p.steps_per - 1) / p.steps_per;
+    p.bytes = p.splits * T * kVals * 4;
+    return p;
+}
+
+hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, int64_t C, float eps,
+                             const SolverOpts& o, hipStream_t stream)
+{
+    const UOut uo{(uint4*)a.u, (uint32_t*)u4.codes, u4.scales};
+    const ReadPlan p = read_plan(T, C);
+    if (p.splits == 0) {
+        const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(read_mix_kernel, dim3((unsigned)((T + kMixTokens - 1) / kMixTokens)),
+                           dim3(kBlock), 0, stream, (const uint4*)a.x, a.H_pre, uo, T, C / 8);
+        return hipGetLastError();
+    }
+    float* partial = static_cast<float*>(a.workspace);
+    hipLaunchKernelGGL(read_part_kernel,
+                       dim3((unsigned)((T + kPartTok - 1) / kPartTok), (unsigned)p.splits),
+                       dim3(kBlock), 0, stream, (const uint16_t*)a.x, (const uint16_t*)a.W, partial,
+                       T, 4 * C, p.steps_per);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (o.solver == 0)
+        hipLaunchKernelGGL(read_finish_kernel<0>, dim3((unsigned)T), dim3(kBlock), 0, stream,
+                           (const uint4*)a.x, partial, (int)p.splits, a.logits, a.rms, a.H_pre,
+                           a.H_post, a.H_res, uo, T, C / 8, eps, o);
+    else
+        hipLaunchKernelGGL(read_finish_kernel<1>, dim3((unsigned)T), dim3(kBlock), 0, stream,
+                           (const uint4*)a.x, partial, (int)p.splits, a.logits, a.rms, a.H_pre,
+                           a.H_post, a.H_res, uo, T, C / 8, eps, o);
+    return hipGetLastError();
+}
+
+}  // namespace mhc

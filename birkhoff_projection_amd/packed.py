@@ -17,7 +17,7 @@ import ctypes
 import torch
 from torch.autograd.function import once_differentiable
 
-from ._lib import LayerCkpt, check, lib
+from ._lib import LayerArgs, LayerCkpt, check, lib
 from .ops import (_bwd_shapes, _dict_out, _fwd_shapes, _layer_args, _need, _out, _ptr, _stream,
                   birkhoff_bwd, make_opts)
 
@@ -316,3 +316,146 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, *, dtype=torch.bfl
         check(lib().mhc_mx4_dequantize(_ptr(codes), _ptr(scales), _ptr(x), dt, R, C,
                                        _stream(codes.device)))
     return x
+
+
+def mx4_matmul(a, b, *, out_dtype=torch.bfloat16, out=None):
+    """a b^T [M, N] for MXFP4 b = (codes, scales) [N, K] and a either such a
+    pair [M, K] or a bf16 / fp32 tensor [M, K], which is quantised as
+    mx4_quantize does.  N is a multiple of 8, K of 32; the sum is fp32."""
+    od = _dtype(out_dtype)
+    bc, bs, N, K = _mx4_given(b, "b")
+    dev = bc.device
+    if isinstance(a, torch.Tensor):
+        ad = _values(a, "a")
+        if a.dim() != 2 or a.shape[1] != K or a.device != dev:
+            raise ValueError(f"a must be [M, {K}] on {dev}, got {tuple(a.shape)} on {a.device}")
+        M = a.shape[0]
+        y = _out(out, "out", out_dtype, (M, N), dev)
+        need = lib().mhc_mx4_matmul_values_workspace_bytes(M, N, K)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+        with torch.cuda.device(dev):
+            check(lib().mhc_mx4_matmul_values(_ptr(a), ad, _ptr(bc), _ptr(bs), _ptr(y), od, M, N, K,
+                                              _ptr(ws), max(need, 0), _stream(dev)))
+        return y
+    ac, as_, M, Ka = _mx4_given(a, "a")
+    if Ka != K or ac.device != dev:
+        raise ValueError(f"a must be [M, {K}] on {dev}, got [{M}, {Ka}] on {ac.device}")
+    y = _out(out, "out", out_dtype, (M, N), dev)
+    with torch.cuda.device(dev):
+        check(lib().mhc_mx4_matmul(_ptr(ac), _ptr(as_), _ptr(bc), _ptr(bs), _ptr(y), od, M, N, K,
+                                   _stream(dev)))
+    return y
+
+
+def mx4_write_back(a, b, x, H_post, H_res, *, out=None, f_out=None):
+    """x_out[t,i] = H_post[t,i] (a b^T)[t] + sum_j H_res[t,i,j] x[t,j] for
+    MXFP4 pairs a [T, K] and b [C, K], x [T,4,C] bf16: the layer function's
+    last product with the layer's write-back in its epilogue.  ``f_out``
+    [T, C] bf16, if given, also receives a b^T."""
+    _need(x, "x", torch.bfloat16)
+    if x.dim() != 3:
+        raise ValueError("x must be [T, n, C]")
+    T, n, C = x.shape
+    dev = x.device
+    ac, as_, M, K = _mx4_given(a, "a")
+    bc, bs, N, Kb = _mx4_given(b, "b")
+    if M != T or N != C or K != Kb or ac.device != dev or bc.device != dev:
+        raise ValueError(f"a and b must be [{T}, K] and [{C}, K] on {dev}, got [{M}, {K}] on "
+                         f"{ac.device} and [{N}, {Kb}] on {bc.device}")
+    for t, name, shape in ((H_post, "H_post", (T, n)), (H_res, "H_res", (T, n, n))):
+        _need(t, name, torch.float32)
+        if tuple(t.shape) != shape or t.device != dev:
+            raise ValueError(f"{name} must be {shape} on {dev}, got {tuple(t.shape)} on {t.device}")
+    y = _out(out, "out", torch.bfloat16, x.shape, dev)
+    if f_out is not None:
+        f_out = _out(f_out, "f_out", torch.bfloat16, (T, C), dev)
+    with torch.cuda.device(dev):
+        check(lib().mhc_mx4_write_back(_ptr(ac), _ptr(as_), _ptr(bc), _ptr(bs), _ptr(x),
+                                       _ptr(H_post), _ptr(H_res), _ptr(y), _ptr(f_out), T, n, C, K,
+                                       _stream(dev)))
+    return y
+
+
+def layer_read(x, W, *, mx4=False, keep_u=False, eps=1e-6, solver="newton", max_iters=None,
+               tol=None, warm_sweeps=None, out=None):
+    """The read half of the layer step: dict(rms, logits, H_pre, H_post,
+    H_res, u) from x [T,4,C] and W [24,4C] bf16.  With ``mx4`` u is the MXFP4
+    pair of the bf16 u (which ``keep_u`` also returns, as "u_values").
+    ``out`` may be a previous result dict."""
+    o = make_opts(solver, max_iters, tol, warm_sweeps)
+    _need(x, "x", torch.bfloat16)
+    if x.dim() != 3:
+        raise ValueError("x must be [T, n, C]")
+    T, n, C = x.shape
+    dev = x.device
+    _need(W, "W", torch.bfloat16)
+    if tuple(W.shape) != (n * n + 2 * n, n * C) or W.device != dev:
+        raise ValueError(f"W must be [n*n+2n, n*C] on {dev}, got {tuple(W.shape)} on {W.device}")
+    out = {} if out is None else out
+    a = LayerArgs()
+    a.T, a.n, a.C, a.eps = T, n, C, float(eps)
+    a.proj = ctypes.pointer(o)
+    a.x, a.W = x.data_ptr(), W.data_ptr()
+    shapes = {k: v for k, v in _fwd_shapes(T, n, C).items() if k not in ("u", "x_out")}
+    r = _dict_out(out, shapes, dev)
+    for name, t in r.items():
+        setattr(a, name, t.data_ptr())
+    codes = scales = None
+    if mx4:
+        codes, scales = (None, None) if out.get("u") is None else out["u"]
+        codes = _out(codes, "u codes", torch.uint8, (T, C // 2), dev)
+        scales = _out(scales, "u scales", torch.uint8, (T, C // BLOCK), dev)
+        r["u"] = (codes, scales)
+    if keep_u or not mx4:
+        key = "u_values" if mx4 else "u"
+        r[key] = _out(out.get(key), key, torch.bfloat16, (T, C), dev)
+        a.u = r[key].data_ptr()
+    need = lib().mhc_layer_read_workspace_bytes(T, n, C)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    a.workspace, a.workspace_bytes = (ws.data_ptr() if ws is not None else None), max(need, 0)
+    with torch.cuda.device(dev):
+        check(lib().mhc_layer_read(ctypes.byref(a), _ptr(codes), _ptr(scales), _stream(dev)))
+    return r
+
+
+class Mx4Linear(torch.autograd.Function):
+    """y = x w^T with every product on MXFP4 operands (see mx4_linear)."""
+
+    @staticmethod
+    def forward(ctx, x, w, format):
+        x, w = x.contiguous(), w.contiguous()
+        y = mx4_matmul(x, mx4_quantize(w), out_dtype=x.dtype)
+        codes, scales = ckpt_pack(x, format=format)
+        ctx.format, ctx.dtype = format, x.dtype
+        ctx.save_for_backward(codes, scales, w)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy):
+        codes, scales, w = ctx.saved_tensors
+        gy = gy.contiguous()
+        gx = gw = None
+        if ctx.needs_input_grad[0]:
+            gx = mx4_matmul(gy, mx4_quantize(w, transpose=True), out_dtype=ctx.dtype)
+        if ctx.needs_input_grad[1] and gy.shape[0] == 0:
+            gw = torch.zeros_like(w)
+        elif ctx.needs_input_grad[1]:
+            x = ckpt_unpack(codes, scales, format=ctx.format, dtype=ctx.dtype)
+            gw = mx4_matmul(mx4_quantize(gy, transpose=True), mx4_quantize(x, transpose=True),
+                            out_dtype=w.dtype)
+        return gx, gw, None
+
+
+def mx4_linear(x, w, *, format="e4m3"):
+    """Differentiable y = x w^T [M, N] for x [M, K], w [N, K] bf16 or fp32 (M,
+    N and K multiples of 32).  Each of the three products takes both operands
+    in MXFP4, quantised along the axis it sums over: y = q(x) q(w)^T,
+    grad_x = q(gy) q(w^T)^T, grad_w = q(gy^T) q(xhat^T)^T.  x is kept for the
+    backward as an 8-bit checkpoint (xhat), w as it is."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be [M, K] and [N, K]")
+    if any(s % BLOCK for s in (*x.shape, *w.shape)):
+        raise ValueError(f"M, N and K must be multiples of {BLOCK}, got x {tuple(x.shape)} and "
+                         f"w {tuple(w.shape)}")
+    return Mx4Linear.apply(x, w, format)

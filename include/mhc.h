@@ -25,6 +25,16 @@
  *   mhc_layer_fwd/bwd   one full mHC residual-layer step (RMSNorm, dynamic
  *                       map, sigmoid read/write maps, projected residual map,
  *                       read-mix and write-back)
+ *   mhc_ckpt_pack/unpack, mhc_stream_mix_ckpt, mhc_stream_mix_bwd_ckpt,
+ *   mhc_layer_fwd_ckpt, mhc_layer_bwd_ckpt
+ *                       activation checkpoints in 8 bits, and the stream mix
+ *                       and the layer step that write them in the forward and
+ *                       read them in the backward
+ *   mhc_layer_read      the read half of the layer step (maps and u)
+ *   mhc_mx4_quantize/dequantize, mhc_mx4_matmul, mhc_mx4_matmul_values,
+ *   mhc_mx4_write_back  microscaled 4-bit quantisation and products for the
+ *                       layer function, the last one with the layer's
+ *                       write-back in its epilogue
  *
  * Sources (cited by page title and section):
  *  - Deep Signal, "DeepSeek mHC: Manifold-Constrained Hyper-Connections"
@@ -73,7 +83,8 @@ extern "C" {
  * makes -1 the default of mhc_proj_opts.max_iters as well (30 Newton
  * iterations, 1000 Sinkhorn sweeps) and bounds every call's batch by
  * MHC_MAX_BATCH / MHC_MAX_TOKENS; 4 adds mhc_birkhoff_pipeline_step and
- * mhc_layer_bwd_noalloc. */
+ * mhc_layer_bwd_noalloc.  Calls added since (checkpoints, 4-bit products,
+ * mhc_layer_read) change nothing that version 4 has and keep its number. */
 #define MHC_ABI_VERSION 4
 
 /* Largest batch one call accepts: B matrices for the projection calls, T
@@ -491,6 +502,52 @@ mhc_status mhc_mx4_quantize(const void* x, int32_t dtype, void* codes, uint8_t* 
                             int64_t C, int32_t transpose, void* stream);
 mhc_status mhc_mx4_dequantize(const void* codes, const uint8_t* scales, void* x, int32_t dtype,
                               int64_t R, int64_t C, void* stream);
+
+/* mhc_mx4_matmul -- out[m,n] = sum_k a[m,k] b[n,k] for MXFP4 a [M,K] and
+ * b [N,K] (both quantised along the summed axis; a weight matrix of a linear
+ * map stored out x in is b).  Products are exact, the sum is fp32, out is
+ * rounded once to bf16 or fp32 (out_dtype).
+ *   M >= 0, N a positive multiple of 8, K a positive multiple of 32
+ *   out [M,N] must not overlap the inputs, which may share memory
+ * mhc_mx4_matmul_values -- the same with a given as bf16 or fp32 values
+ * [M,K], quantised as mhc_mx4_quantize does: in the product's own kernel for
+ * a few rows, otherwise into the workspace first (16-byte aligned, at least
+ * ..._workspace_bytes(M, N, K) bytes; 0 means none is needed; not in use by
+ * another call that overlaps on the device).  For the few-row kernel and the
+ * packed one the sum's order differs, and with it the last bits. */
+mhc_status mhc_mx4_matmul(const void* a_codes, const uint8_t* a_scales, const void* b_codes,
+                          const uint8_t* b_scales, void* out, int32_t out_dtype, int64_t M,
+                          int64_t N, int64_t K, void* stream);
+int64_t mhc_mx4_matmul_values_workspace_bytes(int64_t M, int64_t N, int64_t K);
+mhc_status mhc_mx4_matmul_values(const void* a, int32_t a_dtype, const void* b_codes,
+                                 const uint8_t* b_scales, void* out, int32_t out_dtype, int64_t M,
+                                 int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                                 void* stream);
+
+/* mhc_mx4_write_back -- the last product of the layer function with the
+ * layer's write-back in its epilogue: with f = a b^T (a [T,K], b [C,K], MXFP4),
+ *   x_out[t,i,:] = H_post[t,i] f[t,:] + sum_j H_res[t,i,j] x[t,j,:]
+ * f is used in fp32; f_out, if not NULL, receives it rounded to bf16 [T,C].
+ *   x, x_out  [T, 4, C] bf16;  H_post [T,4], H_res [T,4,4] fp32
+ *   T >= 0, n == 4, C a positive multiple of 8, K of 32; x_out and f_out must
+ *   not overlap another tensor */
+mhc_status mhc_mx4_write_back(const void* a_codes, const uint8_t* a_scales, const void* b_codes,
+                              const uint8_t* b_scales, const void* x, const float* H_post,
+                              const float* H_res, void* x_out, void* f_out, int64_t T, int32_t n,
+                              int64_t C, int64_t K, void* stream);
+
+/* mhc_layer_read -- the read half of the layer step, for when f does not exist
+ * yet: rms, logits, H_pre, H_post, H_res and u from x and W, as mhc_layer_fwd
+ * (f and x_out are ignored).  u goes to a->u (bf16) and, if u_codes and
+ * u_scales are given, also or instead (a->u NULL) to MXFP4 ([T, C/2] and
+ * [T, C/32]): mhc_mx4_quantize of the bf16 u.  Up to 2048 tokens the width is
+ * split over the GPU, with fp32 partial sums in a->workspace (16-byte aligned,
+ * at least mhc_layer_read_workspace_bytes() bytes; 0 means none is needed), and
+ * the sums differ from mhc_layer_fwd's in their order; above that the maps are
+ * mhc_layer_fwd's, bit for bit.  No output may overlap another tensor; the
+ * workspace must not be in use by another call that overlaps on the device. */
+int64_t mhc_layer_read_workspace_bytes(int64_t T, int32_t n, int64_t C);
+mhc_status mhc_layer_read(const mhc_layer_args* a, void* u_codes, uint8_t* u_scales, void* stream);
 
 const char* mhc_status_string(mhc_status s);
 /* Message for the calling thread's last non-OK status ("" if none). */
