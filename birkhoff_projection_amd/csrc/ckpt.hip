@@ -466,7 +466,7 @@ template <int FMT>
 void mix_ckpt_as(const void* x, const float* Hl, float* H_out, void* out, const Packed& ckpt,
                  int64_t T, int64_t C, const SolverOpts* proj, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((T + kTokensPerBlock - 1) / kTokensPerBlock));
+    const dim3 grid(token_grid(T));
     const uint4* xv = static_cast<const uint4*>(x);
     uint4* ov = static_cast<uint4*>(out);
     uint2* cv = static_cast<uint2*>(ckpt.codes);

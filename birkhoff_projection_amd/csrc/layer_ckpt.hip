@@ -70,6 +70,17 @@ MHC_DEV void project_bwd_refined(const float* P, const float* G, float* dA)
     }
 }
 
+// dl / r as an MFMA operand: bf16 parts of 32 tokens' maps,
+// [T / 32][part][map][32 tokens].  The tokens of one product step lie
+// together: with whole rows of tokens per map, 16384 tokens put every map of
+// a step on the same L2 channel (grad_W pass at C = 7168: 186 us, so 167).
+constexpr int kDlParts = 3;
+
+MHC_DEV int64_t dl_at(int64_t t, int part, int map)
+{
+    return ((t >> 5) * kDlParts + part) * (kMaps * 32) + map * 32 + (t & 31);
+}
+
 // ---------------------------------------------------------------------------
 // mix: read-mix u, write-back x_out and the checkpoints of x and f, 16 tokens
 // per workgroup (spaced by the grid size, so the workgroups stream a
@@ -147,13 +158,13 @@ __global__ __launch_bounds__(kBlock) void layer_mix_ckpt_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// dots: wave w of workgroup b handles tokens 64 b + 16 w + [0, 16), one token
-// at a time across the wave; lanes stride over the 8-column chunks.  The
-// (token, chunk) steps of a wave form one software pipeline: step i+1's loads
-// are issued into the other register set before step i is consumed (the
-// vector-memory counter retires in order), across token boundaries too.  At
-// a token's last chunk the 24 partial dots are wave-reduced into LDS; then
-// lanes 0..15 each finish one token.
+// dots: a wave handles tw consecutive tokens (up to 16, fewer where that
+// would leave waves missing), one at a time across the wave; lanes stride over
+// the 8-column chunks.  The (token, chunk) steps of a wave form one software
+// pipeline: step i+1's loads are issued into the other register set before
+// step i is consumed (the vector-memory counter retires in order), across
+// token boundaries too.  At a token's last chunk the 24 partial dots are
+// wave-reduced into LDS; then lanes 0..tw-1 each finish one token.
 // ---------------------------------------------------------------------------
 struct DotsLoads {
     uint2 x[4], f;
@@ -168,18 +179,27 @@ struct DotsLane {
     const uint8_t* fs;
     const uint4* gxo;
     const uint4* gu;
-    int64_t T, C8, nch, tb;
-    int lane;
+    int64_t T, C8, tb;
+    int nch, lane;
 };
 
-MHC_DEV void dots_issue(const DotsLane& L, DotsLoads& d, int64_t i)
+// Place in a wave's sequence of steps: token tl, chunk ci of it.
+struct DotsStep {
+    int tl, ci;
+};
+
+MHC_DEV DotsStep dots_next(const DotsStep& s, int nch)
+{
+    const bool last = s.ci + 1 == nch;
+    return DotsStep{last ? s.tl + 1 : s.tl, last ? 0 : s.ci + 1};
+}
+
+MHC_DEV void dots_issue(const DotsLane& L, DotsLoads& d, const DotsStep& s)
 {
     // steps past the wave's last one read clamped addresses and are never consumed
-    int64_t tl = i / L.nch;
-    tl = tl < 16 ? tl : 15;
-    int64_t t = L.tb + tl;
+    int64_t t = L.tb + s.tl;
     t = t < L.T ? t : L.T - 1;
-    int64_t c = L.lane + 64 * (i % L.nch);
+    int64_t c = L.lane + 64 * (int64_t)s.ci;
     c = c < L.C8 ? c : L.C8 - 1;
     const int64_t cb = L.C8 / 4, b = c >> 2;
 #pragma unroll
@@ -194,12 +214,11 @@ MHC_DEV void dots_issue(const DotsLane& L, DotsLoads& d, int64_t i)
 }
 
 template <int FMT>
-MHC_DEV void dots_consume(const DotsLane& L, const DotsLoads& d, int64_t i, float (&acc)[32],
+MHC_DEV void dots_consume(const DotsLane& L, const DotsLoads& d, const DotsStep& s, float (&acc)[32],
                           float (*sDots)[kMaps])
 {
-    const int64_t tl = i / L.nch, ci = i % L.nch;
-    const int64_t t = L.tb + tl;
-    const int64_t c = L.lane + 64 * ci;
+    const int64_t t = L.tb + s.tl;
+    const int64_t c = L.lane + 64 * (int64_t)s.ci;
     if (t < L.T && c < L.C8) {
         float sc[4];
 #pragma unroll
@@ -237,10 +256,10 @@ MHC_DEV void dots_consume(const DotsLane& L, const DotsLoads& d, int64_t i, floa
             }
         }
     }
-    if (ci == L.nch - 1) {  // the token's last chunk: reduce its dots
+    if (s.ci == L.nch - 1) {  // the token's last chunk: reduce its dots
         const float sm = wave_sum_halving<32>(acc);
         const int idx = (L.lane >> 1) & 31;
-        if ((L.lane & 1) == 0 && idx < kMaps) sDots[tl][idx] = sm;
+        if ((L.lane & 1) == 0 && idx < kMaps) sDots[s.tl][idx] = sm;
 #pragma unroll
         for (int k = 0; k < 32; ++k) acc[k] = 0.f;
     }
@@ -252,33 +271,35 @@ __global__ __launch_bounds__(kBlock) void layer_dots_ckpt_kernel(
     const uint8_t* __restrict__ fs, const uint4* __restrict__ gxo, const uint4* __restrict__ gu,
     const float* __restrict__ Hpre, const float* __restrict__ Hpost, const float* __restrict__ Hres,
     const float* __restrict__ logits, const float* __restrict__ rms, float* __restrict__ glogits,
-    float* __restrict__ svec, __bf16* __restrict__ dlT, int64_t T, int64_t Tp, int64_t C8)
+    float* __restrict__ svec, __bf16* __restrict__ dlT, int64_t T, int64_t Tp, int64_t C8, int tw)
 {
     __shared__ float sDots[4][16][kMaps];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t tb = (int64_t)blockIdx.x * 64 + 16 * w;
+    const int64_t tb = ((int64_t)blockIdx.x * 4 + w) * tw;
     DotsLane L;
     L.xc = xc; L.xs = xs; L.fc = fc; L.fs = fs; L.gxo = gxo; L.gu = gu;
-    L.T = T; L.C8 = C8; L.nch = (C8 + 63) / 64; L.tb = tb; L.lane = lane;
+    L.T = T; L.C8 = C8; L.nch = (int)((C8 + 63) / 64); L.tb = tb; L.lane = lane;
     float acc[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-    // 16 tokens x nch chunks: always an even number of steps
-    const int64_t steps = 16 * L.nch;
+    // the steps are taken in pairs; an odd last one has tl = tw and does nothing
     DotsLoads d0, d1;
-    dots_issue(L, d0, 0);
-    for (int64_t i = 0; i < steps; i += 2) {
-        dots_issue(L, d1, i + 1);
+    DotsStep s0{0, 0};
+    dots_issue(L, d0, s0);
+    while (s0.tl < tw) {
+        const DotsStep s1 = dots_next(s0, L.nch), s2 = dots_next(s1, L.nch);
+        dots_issue(L, d1, s1);
         __builtin_amdgcn_sched_barrier(0);
-        dots_consume<FMT>(L, d0, i, acc, sDots[w]);
+        dots_consume<FMT>(L, d0, s0, acc, sDots[w]);
         __builtin_amdgcn_sched_barrier(0);
-        dots_issue(L, d0, i + 2);
+        dots_issue(L, d0, s2);
         __builtin_amdgcn_sched_barrier(0);
-        dots_consume<FMT>(L, d1, i + 1, acc, sDots[w]);
+        if (s1.tl < tw) dots_consume<FMT>(L, d1, s1, acc, sDots[w]);
         __builtin_amdgcn_sched_barrier(0);
+        s0 = s2;
     }
     __syncthreads();
-    if (lane >= 16) return;
+    if (lane >= tw) return;
     const int64_t t = tb + lane;
     if (t >= Tp) return;
     float dl[kMaps];
@@ -327,7 +348,7 @@ __global__ __launch_bounds__(kBlock) void layer_dots_ckpt_kernel(
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
             const __bf16 h = (__bf16)v;
-            dlT[((int64_t)p * kMaps + m) * Tp + t] = h;
+            dlT[dl_at(t, p, m)] = h;
             v -= (float)h;
         }
     }
@@ -521,8 +542,8 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
 }
 
 // ---------------------------------------------------------------------------
-// dw: workgroup = 128 flattened k x one token group; wave w takes every 4th
-// 32-token chunk of the group:
+// dw: workgroup = 256 flattened k x one token group; two waves take one half
+// of the columns each, and every 2nd 32-token chunk of the group:
 //   dW^T tile (32 maps x 16 k) += dlT (32 maps x 32 tokens) * xhat (32 tokens x 16 k)
 // The MFMA B operand wants 8 consecutive tokens of one k per lane, the memory
 // holds 8 consecutive k of one token.  A lane loads 8 k of 8 tokens (16 lanes
@@ -532,15 +553,14 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
 // 16 consecutive k, which only relabels the columns of the result.  So the
 // tile never passes through LDS.  The three bf16 parts of dlT (A, from L2)
 // are issued with the codes, one chunk ahead, into the other of two register
-// sets.  The four waves' partials are summed in LDS and one partial per token
-// group is written, in a fixed order throughout.
+// sets.  The two partials of each column are summed in LDS and one partial per
+// token group is written, in a fixed order throughout.
 // ---------------------------------------------------------------------------
-constexpr int kDwK = 128;         // flattened k per workgroup
+constexpr int kDwK = 128;         // flattened k per wave, half a workgroup's
 constexpr int kDwNt = kDwK / 16;  // MFMA tiles
-constexpr int kDwParts = 3;       // bf16 parts of dl / r
 
 struct DwLoads {
-    uint4 a[kDwParts][2];  // dlT parts: maps 16 mt + row, tokens 8 kq ..+7
+    uint4 a[kDlParts][2];  // dlT parts: maps 16 mt + row, tokens 8 kq ..+7
     uint2 x[8];            // codes of token 8 kq + e, k 8 row ..+7
     uint32_t s[8];
 };
@@ -556,8 +576,8 @@ MHC_DEV void dw_issue(DwLoads& d, const uint8_t* __restrict__ xc, const uint8_t*
     for (int mt = 0; mt < 2; ++mt) {
         const int m = 16 * mt + row < kMaps ? 16 * mt + row : kMaps - 1;
 #pragma unroll
-        for (int p = 0; p < kDwParts; ++p)
-            d.a[p][mt] = *reinterpret_cast<const uint4*>(dlT + ((int64_t)p * kMaps + m) * Tp + ta + 8 * kq);
+        for (int p = 0; p < kDlParts; ++p)
+            d.a[p][mt] = *reinterpret_cast<const uint4*>(dlT + dl_at(ta, p, m) + 8 * kq);
     }
     const int64_t k = k0 + 8 * row;
 #pragma unroll
@@ -591,7 +611,7 @@ MHC_DEV void dw_consume(const DwLoads& d, floatx4 (&acc)[2][kDwNt], bool live)
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int p = kDwParts - 1; p >= 0; --p)
+                for (int p = kDlParts - 1; p >= 0; --p)
                     acc[mt][4 * h + q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                         as_bf16x8(d.a[p][mt]), bb, acc[mt][4 * h + q], 0, 0, 0);
         }
@@ -603,11 +623,12 @@ __global__ __launch_bounds__(kBlock) void layer_dw_ckpt_kernel(
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, const __bf16* __restrict__ dlT,
     float* __restrict__ partial, int64_t T, int64_t Tp, int64_t C, int64_t group_tokens)
 {
-    __shared__ float sR[32][kDwK + 1];
+    __shared__ __attribute__((aligned(16))) float sR[4][kMaps][kDwK + 4];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int row = lane & 15, kq = lane >> 4;
     const int64_t D = 4 * C;
-    const int64_t k0 = (int64_t)blockIdx.x * kDwK;
+    const int half = w & 1, phase = w >> 1;
+    const int64_t k0 = (int64_t)blockIdx.x * (2 * kDwK) + kDwK * half;
     const int64_t g = blockIdx.y;
     const int64_t tg0 = g * group_tokens;
     int64_t tg1 = tg0 + group_tokens;
@@ -618,37 +639,39 @@ __global__ __launch_bounds__(kBlock) void layer_dw_ckpt_kernel(
 #pragma unroll
         for (int nt = 0; nt < kDwNt; ++nt) acc[mt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
     DwLoads d0, d1;
-    const int64_t first = tg0 + 32 * w;
+    const int64_t first = tg0 + 32 * phase;
     dw_issue(d0, xc, xs, dlT, first, T, Tp, D, k0, lane);
-    for (int64_t tc = first; tc < tg1; tc += 256) {
-        dw_issue(d1, xc, xs, dlT, tc + 128, T, Tp, D, k0, lane);
+    for (int64_t tc = first; tc < tg1; tc += 128) {
+        dw_issue(d1, xc, xs, dlT, tc + 64, T, Tp, D, k0, lane);
         __builtin_amdgcn_sched_barrier(0);
         dw_consume<FMT>(d0, acc, true);
         __builtin_amdgcn_sched_barrier(0);
-        dw_issue(d0, xc, xs, dlT, tc + 256, T, Tp, D, k0, lane);
+        dw_issue(d0, xc, xs, dlT, tc + 128, T, Tp, D, k0, lane);
         __builtin_amdgcn_sched_barrier(0);
-        dw_consume<FMT>(d1, acc, tc + 128 < tg1);
+        dw_consume<FMT>(d1, acc, tc + 64 < tg1);
         __builtin_amdgcn_sched_barrier(0);
     }
-    // sum the four waves' partials: wave 0 writes, the others add in turn
-    for (int ww = 0; ww < 4; ++ww) {
-        if (w == ww) {
+    // the two partials of each column, summed in order
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                for (int nt = 0; nt < kDwNt; ++nt)
+        for (int v = 0; v < 4; ++v) {
+            const int m = 16 * mt + 4 * kq + v;
+            if (m < kMaps) {
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        float& dst = sR[16 * mt + 4 * kq + v][8 * row + nt];
-                        dst = (ww == 0 ? 0.f : dst) + acc[mt][nt][v];
-                    }
+                for (int nt = 0; nt < kDwNt; nt += 4)
+                    *reinterpret_cast<floatx4*>(&sR[w][m][8 * row + nt]) =
+                        floatx4{acc[mt][nt][v], acc[mt][nt + 1][v], acc[mt][nt + 2][v], acc[mt][nt + 3][v]};
+            }
         }
-        __syncthreads();
-    }
+    __syncthreads();
     float* out = partial + g * (int64_t)kMaps * D;
-    for (int p = threadIdx.x; p < kMaps * kDwK; p += kBlock) {
-        const int m = p / kDwK, kk = p % kDwK;
-        out[m * D + k0 + kk] = sR[m][kk];
+    for (int p = threadIdx.x; p < kMaps * 2 * kDwK / 4; p += kBlock) {
+        const int m = p / (2 * kDwK / 4), kk = 4 * (p % (2 * kDwK / 4));
+        const int h = kk / kDwK, c = kk % kDwK;
+        const floatx4 s = *reinterpret_cast<const floatx4*>(&sR[h][m][c]) +
+                          *reinterpret_cast<const floatx4*>(&sR[2 + h][m][c]);
+        *reinterpret_cast<floatx4*>(&out[m * D + (int64_t)blockIdx.x * (2 * kDwK) + kk]) = s;
     }
 }
 
@@ -663,10 +686,12 @@ hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, in
     uint4* wt = reinterpret_cast<uint4*>(ws + p.off_wt);
     float* partial = reinterpret_cast<float*>(ws + p.off_partial);
     const uint2* xc = static_cast<const uint2*>(x.codes);
-    hipLaunchKernelGGL(layer_dots_ckpt_kernel<FMT>, dim3((unsigned)(p.Tp / 64)), dim3(kBlock), 0,
+    int tw = 16;  // tokens per wave: a workgroup for every compute unit where there are as many tokens
+    while (tw > 1 && p.Tp / (4 * tw) < 256) tw /= 2;
+    hipLaunchKernelGGL(layer_dots_ckpt_kernel<FMT>, dim3((unsigned)(p.Tp / (4 * tw))), dim3(kBlock), 0,
                        stream, xc, x.scales, static_cast<const uint2*>(f.codes), f.scales,
                        (const uint4*)a.grad_x_out, (const uint4*)a.grad_u, a.H_pre, a.H_post,
-                       a.H_res, a.logits, a.rms, a.grad_logits, svec, dlT, T, p.Tp, C / 8);
+                       a.H_res, a.logits, a.rms, a.grad_logits, svec, dlT, T, p.Tp, C / 8, tw);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     e = launch_layer_wt(a.W, wt, C, stream);
@@ -677,7 +702,7 @@ hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, in
                        svec, (uint4*)a.grad_x, (uint4*)a.grad_f, T, C);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(layer_dw_ckpt_kernel<FMT>, dim3((unsigned)(4 * C / kDwK), (unsigned)p.groups),
+    hipLaunchKernelGGL(layer_dw_ckpt_kernel<FMT>, dim3((unsigned)(4 * C / (2 * kDwK)), (unsigned)p.groups),
                        dim3(kBlock), 0, stream, (const uint8_t*)x.codes, x.scales, dlT, partial, T,
                        p.Tp, C, p.group_tokens);
     e = hipGetLastError();
@@ -689,7 +714,7 @@ template <int FMT>
 hipError_t layer_mix_as(const LayerPtrs& a, const Packed& x, const Packed& f, int64_t T, int64_t C,
                         hipStream_t stream)
 {
-    hipLaunchKernelGGL(layer_mix_ckpt_kernel<FMT>, dim3((unsigned)((T + kMixTokens - 1) / kMixTokens)),
+    hipLaunchKernelGGL(layer_mix_ckpt_kernel<FMT>, dim3(token_grid(T)),
                        dim3(kBlock), 0, stream, (const uint4*)a.x, (const uint4*)a.f, a.H_pre,
                        a.H_post, a.H_res, (uint4*)a.u, (uint4*)a.x_out, (uint2*)x.codes, x.scales,
                        (uint2*)f.codes, f.scales, T, C / 8);
@@ -708,7 +733,7 @@ LayerCkptPlan layer_ckpt_plan(int64_t T, int64_t C)
     const int64_t D = 4 * C;
     p.off_s = 0;
     p.off_dl = (p.Tp * 4 + 255) / 256 * 256;
-    p.off_wt = p.off_dl + (p.Tp * kMaps * 2 * kDwParts + 255) / 256 * 256;
+    p.off_wt = p.off_dl + (p.Tp * kMaps * 2 * kDlParts + 255) / 256 * 256;
     p.off_partial = p.off_wt + (D * kMaps * 2 + 255) / 256 * 256;
     p.bytes = p.off_partial + p.groups * kMaps * D * 4;
     return p;

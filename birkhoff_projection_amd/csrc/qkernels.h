@@ -10,6 +10,14 @@
 
 namespace mhc {
 
+// Workgroups of the passes that take tokens b, b + G, ... (at most 16 each): 16
+// tokens per workgroup, fewer where that would leave most of the chip idle.
+inline unsigned token_grid(int64_t T)
+{
+    const int64_t full = (T + 15) / 16, most = T < 1024 ? T : 1024;
+    return (unsigned)(full > most ? full : most);
+}
+
 // A packed tensor: codes and one scale byte per block of 32 columns of a row.
 struct Packed {
     void* codes;
@@ -64,7 +72,7 @@ ReadPlan read_plan(int64_t T, int64_t C);
 hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, int64_t C, float eps,
                              const SolverOpts& o, hipStream_t stream);
 
-// Backward workspace: s[Tp] fp32 | dl^T / r in three bf16 parts [3][24][Tp] |
+// Backward workspace: s[Tp] fp32 | dl / r in bf16 parts [Tp/32][3][24][32] |
 // W^T [4C][24] bf16 | grad_W partials [groups][24][4C] fp32 (each 256-byte
 // aligned).
 struct LayerCkptPlan {

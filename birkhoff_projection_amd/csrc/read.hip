@@ -237,7 +237,7 @@ hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, in
     if (p.splits == 0) {
         const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(read_mix_kernel, dim3((unsigned)((T + kMixTokens - 1) / kMixTokens)),
+        hipLaunchKernelGGL(read_mix_kernel, dim3(token_grid(T)),
                            dim3(kBlock), 0, stream, (const uint4*)a.x, a.H_pre, uo, T, C / 8);
         return hipGetLastError();
     }

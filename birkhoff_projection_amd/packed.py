@@ -18,12 +18,41 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._lib import LayerArgs, LayerCkpt, check, lib
-from .ops import (_bwd_shapes, _dict_out, _fwd_shapes, _layer_args, _need, _out, _ptr, _stream,
-                  birkhoff_bwd, make_opts)
+from .ops import (_bwd_shapes, _dict_out, _fwd_shapes, _layer_args, _need, _out, birkhoff_bwd,
+                  make_opts)
 
 FORMATS = {"e4m3": 0, "int8": 1}
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 BLOCK = 32
+
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(device, fn, *args):
+    """fn(*args, stream) on ``device`` and its current stream.  Small calls
+    last a few microseconds, as long as the marshalling around them: the
+    stream handle is taken without a Stream object, and the device is switched
+    only if it is not the current one."""
+    i = device.index
+    if i == _current_device():
+        status = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, _raw_stream(i))
+    if status:
+        check(status)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _opts(solver, max_iters, tol, warm_sweeps):
+    """Solver options, None (the call's defaults) where nothing is chosen."""
+    if solver == "newton" and max_iters is None and tol is None and warm_sweeps is None:
+        return None
+    return make_opts(solver, max_iters, tol, warm_sweeps)
 
 
 def _format(format):
@@ -75,9 +104,8 @@ def ckpt_pack(x: torch.Tensor, *, format="e4m3", out=None):
         raise ValueError("x must be [..., C]")
     C = x.shape[-1]
     codes, scales = _pair(out, "out", x.shape, x.device)
-    with torch.cuda.device(x.device):
-        check(lib().mhc_ckpt_pack(_ptr(x), dt, _ptr(codes), _ptr(scales),
-                                  x.numel() // max(C, 1), C, fmt, _stream(x.device)))
+    _call(x.device, lib().mhc_ckpt_pack, _ptr(x), dt, _ptr(codes), _ptr(scales),
+          x.numel() // max(C, 1), C, fmt)
     return codes, scales
 
 
@@ -91,9 +119,8 @@ def ckpt_unpack(codes: torch.Tensor, scales: torch.Tensor, *, format="e4m3",
     _given((codes, scales), "checkpoint", codes.shape, codes.device)
     C = codes.shape[-1]
     x = _out(out, "out", dtype, codes.shape, codes.device)
-    with torch.cuda.device(codes.device):
-        check(lib().mhc_ckpt_unpack(_ptr(codes), _ptr(scales), _ptr(x), dt,
-                                    codes.numel() // max(C, 1), C, fmt, _stream(codes.device)))
+    _call(codes.device, lib().mhc_ckpt_unpack, _ptr(codes), _ptr(scales), _ptr(x), dt,
+          codes.numel() // max(C, 1), C, fmt)
     return x
 
 
@@ -127,13 +154,11 @@ def stream_mix_ckpt(x: torch.Tensor, H: torch.Tensor = None, *, logits: torch.Te
     elif return_H:
         H_out = H
     codes, scales = _pair(ckpt, "ckpt", x.shape, x.device)
+    # a NULL proj means "H is given", so the projecting form always passes options
     o = make_opts(solver, max_iters, tol, warm_sweeps) if logits is not None else None
-    with torch.cuda.device(x.device):
-        check(lib().mhc_stream_mix_ckpt(_ptr(x), _ptr(src),
-                                        _ptr(H_out) if logits is not None else None, _ptr(y),
-                                        _ptr(codes), _ptr(scales), T, n, C, fmt,
-                                        ctypes.byref(o) if o is not None else None,
-                                        _stream(x.device)))
+    _call(x.device, lib().mhc_stream_mix_ckpt, _ptr(x), _ptr(src),
+          _ptr(H_out) if logits is not None else None, _ptr(y), _ptr(codes), _ptr(scales), T, n, C,
+          fmt, ctypes.byref(o) if o is not None else None)
     return (y, H_out, (codes, scales)) if return_H else (y, (codes, scales))
 
 
@@ -151,9 +176,8 @@ def stream_mix_bwd_ckpt(ckpt, H: torch.Tensor, grad_out: torch.Tensor, *, format
     gx, gH = (None, None) if out is None else out
     gx = _out(gx, "grad_x", torch.bfloat16, grad_out.shape, dev)
     gH = _out(gH, "grad_H", torch.float32, H.shape, dev)
-    with torch.cuda.device(dev):
-        check(lib().mhc_stream_mix_bwd_ckpt(_ptr(codes), _ptr(scales), _ptr(H), _ptr(grad_out),
-                                            _ptr(gx), _ptr(gH), T, n, C, fmt, _stream(dev)))
+    _call(dev, lib().mhc_stream_mix_bwd_ckpt, _ptr(codes), _ptr(scales), _ptr(H),
+          _ptr(grad_out), _ptr(gx), _ptr(gH), T, n, C, fmt)
     return gx, gH
 
 
@@ -205,16 +229,14 @@ def layer_fwd_ckpt(x, W, f, *, format="e4m3", eps=1e-6, solver="newton", max_ite
     (forward dict, dict(x=(codes, scales), f=(codes, scales))); the forward's
     outputs are layer_fwd's bit for bit.  Only the checkpoints and the
     forward's rms, logits and maps are needed by layer_bwd_ckpt."""
-    o = make_opts(solver, max_iters, tol, warm_sweeps)
-    a = _layer_args(x, W, f, eps, o)
+    a = _layer_args(x, W, f, eps, _opts(solver, max_iters, tol, warm_sweeps))
     T, n, C = x.shape
     dev = x.device
     k, ckpt = _ckpt_args(ckpt, T, n, C, dev, format, True)
     out = _dict_out(out, _fwd_shapes(T, n, C), dev)
     for name, t in out.items():
         setattr(a, name, t.data_ptr())
-    with torch.cuda.device(dev):
-        check(lib().mhc_layer_fwd_ckpt(ctypes.byref(a), ctypes.byref(k), _stream(dev)))
+    _call(dev, lib().mhc_layer_fwd_ckpt, ctypes.byref(a), ctypes.byref(k))
     return out, ckpt
 
 
@@ -263,8 +285,7 @@ def layer_bwd_ckpt(ckpt, W, fwd, grad_x_out, grad_u, *, format="e4m3", workspace
     a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
     if T == 0:
         out["grad_W"].zero_()  # a sum over no tokens; the call enqueues nothing
-    with torch.cuda.device(dev):
-        check(lib().mhc_layer_bwd_ckpt(ctypes.byref(a), ctypes.byref(k), _stream(dev)))
+    _call(dev, lib().mhc_layer_bwd_ckpt, ctypes.byref(a), ctypes.byref(k))
     return out
 
 
@@ -287,9 +308,8 @@ def mx4_quantize(x: torch.Tensor, *, transpose=False, out=None):
     codes, scales = (None, None) if out is None else out
     codes = _out(codes, "codes", torch.uint8, (rows, cols // 2), x.device)
     scales = _out(scales, "scales", torch.uint8, (rows, cols // BLOCK), x.device)
-    with torch.cuda.device(x.device):
-        check(lib().mhc_mx4_quantize(_ptr(x), dt, _ptr(codes), _ptr(scales), R, C,
-                                     1 if transpose else 0, _stream(x.device)))
+    _call(x.device, lib().mhc_mx4_quantize, _ptr(x), dt, _ptr(codes), _ptr(scales), R, C,
+          int(bool(transpose)))
     return codes, scales
 
 
@@ -312,9 +332,7 @@ def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, *, dtype=torch.bfl
     dt = _dtype(dtype)
     codes, scales, R, C = _mx4_given((codes, scales), "quantised")
     x = _out(out, "out", dtype, (R, C), codes.device)
-    with torch.cuda.device(codes.device):
-        check(lib().mhc_mx4_dequantize(_ptr(codes), _ptr(scales), _ptr(x), dt, R, C,
-                                       _stream(codes.device)))
+    _call(codes.device, lib().mhc_mx4_dequantize, _ptr(codes), _ptr(scales), _ptr(x), dt, R, C)
     return x
 
 
@@ -333,17 +351,15 @@ def mx4_matmul(a, b, *, out_dtype=torch.bfloat16, out=None):
         y = _out(out, "out", out_dtype, (M, N), dev)
         need = lib().mhc_mx4_matmul_values_workspace_bytes(M, N, K)
         ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-        with torch.cuda.device(dev):
-            check(lib().mhc_mx4_matmul_values(_ptr(a), ad, _ptr(bc), _ptr(bs), _ptr(y), od, M, N, K,
-                                              _ptr(ws), max(need, 0), _stream(dev)))
+        _call(dev, lib().mhc_mx4_matmul_values, _ptr(a), ad, _ptr(bc), _ptr(bs), _ptr(y), od, M, N,
+              K, _ptr(ws), max(need, 0))
         return y
     ac, as_, M, Ka = _mx4_given(a, "a")
     if Ka != K or ac.device != dev:
         raise ValueError(f"a must be [M, {K}] on {dev}, got [{M}, {Ka}] on {ac.device}")
     y = _out(out, "out", out_dtype, (M, N), dev)
-    with torch.cuda.device(dev):
-        check(lib().mhc_mx4_matmul(_ptr(ac), _ptr(as_), _ptr(bc), _ptr(bs), _ptr(y), od, M, N, K,
-                                   _stream(dev)))
+    _call(dev, lib().mhc_mx4_matmul, _ptr(ac), _ptr(as_), _ptr(bc), _ptr(bs), _ptr(y), od, M, N,
+          K)
     return y
 
 
@@ -369,10 +385,8 @@ def mx4_write_back(a, b, x, H_post, H_res, *, out=None, f_out=None):
     y = _out(out, "out", torch.bfloat16, x.shape, dev)
     if f_out is not None:
         f_out = _out(f_out, "f_out", torch.bfloat16, (T, C), dev)
-    with torch.cuda.device(dev):
-        check(lib().mhc_mx4_write_back(_ptr(ac), _ptr(as_), _ptr(bc), _ptr(bs), _ptr(x),
-                                       _ptr(H_post), _ptr(H_res), _ptr(y), _ptr(f_out), T, n, C, K,
-                                       _stream(dev)))
+    _call(dev, lib().mhc_mx4_write_back, _ptr(ac), _ptr(as_), _ptr(bc), _ptr(bs), _ptr(x),
+          _ptr(H_post), _ptr(H_res), _ptr(y), _ptr(f_out), T, n, C, K)
     return y
 
 
@@ -382,7 +396,7 @@ def layer_read(x, W, *, mx4=False, keep_u=False, eps=1e-6, solver="newton", max_
     H_res, u) from x [T,4,C] and W [24,4C] bf16.  With ``mx4`` u is the MXFP4
     pair of the bf16 u (which ``keep_u`` also returns, as "u_values").
     ``out`` may be a previous result dict."""
-    o = make_opts(solver, max_iters, tol, warm_sweeps)
+    o = _opts(solver, max_iters, tol, warm_sweeps)
     _need(x, "x", torch.bfloat16)
     if x.dim() != 3:
         raise ValueError("x must be [T, n, C]")
@@ -394,7 +408,7 @@ def layer_read(x, W, *, mx4=False, keep_u=False, eps=1e-6, solver="newton", max_
     out = {} if out is None else out
     a = LayerArgs()
     a.T, a.n, a.C, a.eps = T, n, C, float(eps)
-    a.proj = ctypes.pointer(o)
+    a.proj = ctypes.pointer(o) if o is not None else None
     a.x, a.W = x.data_ptr(), W.data_ptr()
     shapes = {k: v for k, v in _fwd_shapes(T, n, C).items() if k not in ("u", "x_out")}
     r = _dict_out(out, shapes, dev)
@@ -413,8 +427,7 @@ def layer_read(x, W, *, mx4=False, keep_u=False, eps=1e-6, solver="newton", max_
     need = lib().mhc_layer_read_workspace_bytes(T, n, C)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
     a.workspace, a.workspace_bytes = (ws.data_ptr() if ws is not None else None), max(need, 0)
-    with torch.cuda.device(dev):
-        check(lib().mhc_layer_read(ctypes.byref(a), _ptr(codes), _ptr(scales), _stream(dev)))
+    _call(dev, lib().mhc_layer_read, ctypes.byref(a), _ptr(codes), _ptr(scales))
     return r
 
 
