@@ -106,44 +106,26 @@ constexpr int kTK = 256;
 constexpr int kRowBytes = kTK / 2;
 constexpr int kBlock = 256;
 
-// ROWS rows of 128 bytes from row0 of a matrix of `n` rows of Kb bytes,
-// straight to LDS; rows past n and bytes past Kb repeat the last ones (their
-// products are not used).  The copy instruction takes a wave-uniform LDS
-// address and writes 16 bytes per lane behind it; it is written as assembly
-// because the compiler, which cannot tell the two buffers apart, would wait
-// for all copies before every LDS read.  It has no register result; the wait
-// is the vmcnt(0) before the barrier that hands the buffer over.
-template <int ROWS>
-MHC_DEV void stage_codes(const uint8_t* __restrict__ src, int64_t row0, int64_t n, int64_t Kb,
-                         int64_t kb0, uint32_t lds, int tid)
+// One copy of 16 bytes per lane from global memory straight to LDS: from a
+// wave-uniform base plus a lane offset to a wave-uniform LDS address plus 16
+// bytes per lane.  It is written as assembly because the compiler, which
+// cannot tell the two buffers apart, would wait for all copies before every
+// LDS read.  It has no register result; the wait is the vmcnt(0) before the
+// barrier that hands the buffer over.
+MHC_DEV void copy_to_lds(const uint8_t* base, uint32_t off, uint32_t lds)
 {
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-#pragma unroll
-    for (int i = 0; i < ROWS * 8 / kBlock; ++i) {
-        const int p = kBlock * i + tid;           // 16-byte place in LDS
-        const int r = p >> 3, c = (p & 7) ^ (r & 7);
-        int64_t row = row0 + r;
-        row = row < n ? row : n - 1;
-        int64_t kb = kb0 + 16 * c;
-        kb = kb < Kb ? kb : Kb - 16;
-        const uint8_t* g = src + row * Kb + kb;
-        const uint32_t l = lds + 16 * (kBlock * i + 64 * w);
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                     :: "s"(l), "v"(g) : "memory", "m0");
-    }
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
 
 struct ScaleRegs {
     uint32_t lo, hi;
 };
 
-// the 8 scale bytes of one row's stage
+// the 8 scale bytes of one row's stage; `left` of them exist
 template <bool TAIL>
-MHC_DEV ScaleRegs load_scales(const uint8_t* __restrict__ s, int64_t row, int64_t n, int64_t Ks,
-                              int64_t ks0)
+MHC_DEV ScaleRegs load_scales(const uint8_t* p, int64_t left)
 {
-    row = row < n ? row : n - 1;
-    const uint8_t* p = s + row * Ks + ks0;
     ScaleRegs r;
     if (!TAIL) {
         const uint2 v = *reinterpret_cast<const uint2*>(p);
@@ -152,7 +134,7 @@ MHC_DEV ScaleRegs load_scales(const uint8_t* __restrict__ s, int64_t row, int64_
     } else {
         uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = ks0 + i < Ks ? p[i] : 127u;
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 127u;
         r.lo = v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24;
         r.hi = v[4] | v[5] << 8 | v[6] << 16 | v[7] << 24;
     }
@@ -189,15 +171,21 @@ MHC_DEV void read_frags(Frags<TM, TN>& f, const uint8_t* sA, const uint8_t* sB, 
 }
 
 template <int S, int TM, int TN>
+MHC_DEV void mma_one(const Frags<TM, TN>& f, const uint32_t (&xa)[TM], const uint32_t (&xb)[TN],
+                     f32x16 (&acc)[TM][TN], int i, int j)
+{
+    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        frag(f.a[i]), frag(f.b[j]), acc[i][j], kFp4, kFp4, S, (int)xa[i], S, (int)xb[j]);
+}
+
+template <int S, int TM, int TN>
 MHC_DEV void mma_step(const Frags<TM, TN>& f, const uint32_t (&xa)[TM], const uint32_t (&xb)[TN],
                       f32x16 (&acc)[TM][TN])
 {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                frag(f.a[i]), frag(f.b[j]), acc[i][j], kFp4, kFp4, S, (int)xa[i], S, (int)xb[j]);
+        for (int j = 0; j < TN; ++j) mma_one<S>(f, xa, xb, acc, i, j);
 }
 
 template <int TM, int TN, int EPI, bool TAIL>
@@ -209,7 +197,7 @@ __global__ __launch_bounds__(kBlock) void mx4_tile_kernel(Mx4Args p, unsigned gm
     static_assert(4 * 32 * kPitch * 4 <= 2 * kBytes, "output strips fit the stage buffers");
     __shared__ __attribute__((aligned(16))) uint8_t sC[2][kBytes];
     __shared__ __attribute__((aligned(8))) uint32_t sX[2][2 * (BM + BN)];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // Workgroups go to the 8 dies in turn; each die takes a run of
     // consecutive tiles, in bands of 4 tile rows, so that the rows and columns
     // its workgroups share stay in its cache.
@@ -220,13 +208,77 @@ __global__ __launch_bounds__(kBlock) void mx4_tile_kernel(Mx4Args p, unsigned gm
         unsigned t = die * per + (die < extra ? die : extra) + id / 8;
         const unsigned band = t / (4 * gn), rows = gm - 4 * band < 4 ? gm - 4 * band : 4;
         t -= 4 * gn * band;
-        tm = 4 * band + t % rows;
-        tn = t / rows;
+        // (divisions run on the vector unit; the tile is the wave's own again)
+        tm = __builtin_amdgcn_readfirstlane(4 * band + t % rows);
+        tn = __builtin_amdgcn_readfirstlane(t / rows);
     }
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int64_t Kb = p.K / 2, Ks = p.K / 32;
     const int ra = 32 * TM * (w & 1) + (lane & 31), rb = 32 * TN * (w >> 1) + (lane & 31);
     const int kh = lane >> 5;
+    const int stages = (int)((p.K + kTK - 1) / kTK);
+
+    // A thread copies piece c of rows 32 i + tid / 8 (its place in LDS is fixed
+    // by tid).  Rows past the matrix repeat its last one; their products are
+    // not used.  Row offsets fit 32 bits: 255 rows of at most 2^23 bytes.
+    constexpr int NA = 2 * TM, NB = 2 * TN;  // copies per thread and stage
+    const int c16 = 16 * ((tid & 7) ^ ((tid >> 3) & 7));
+    const uint8_t* baseA = p.a + m0 * Kb;
+    const uint8_t* baseB = p.b + n0 * Kb;
+    uint32_t offA[NA], offB[NB];
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+        const int64_t r = 32 * i + (tid >> 3), last = p.M - 1 - m0;
+        offA[i] = (uint32_t)((r < last ? r : last) * Kb) + c16;
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int64_t r = 32 * i + (tid >> 3), last = p.N - 1 - n0;
+        offB[i] = (uint32_t)((r < last ? r : last) * Kb) + c16;
+    }
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sC[0][0];
+    const auto copy = [&](int st, int buf, int i) {  // copy i of stage st
+        uint32_t cut = 0;
+        if (TAIL) {  // bytes past the row repeat its last piece
+            const int64_t over = (int64_t)st * kRowBytes + c16 - (Kb - 16);
+            cut = over > 0 ? (uint32_t)over : 0u;
+        }
+        const bool isA = i < NA;
+        const uint8_t* base = (isA ? baseA : baseB) + (int64_t)st * kRowBytes;
+        copy_to_lds(base, (isA ? offA[isA ? i : 0] : offB[isA ? 0 : i - NA]) - cut,
+                    lds0 + buf * kBytes + 16 * (kBlock * i + 64 * w));
+    };
+    // scale rows of this thread: row tid + 256 i of A's then B's (a workgroup
+    // with fewer rows than threads loads some twice)
+    constexpr int SR = (BM + BN + kBlock - 1) / kBlock;
+    const uint8_t* sp[SR];
+    int sr[SR];
+#pragma unroll
+    for (int i = 0; i < SR; ++i) {
+        sr[i] = (tid + kBlock * i) % (BM + BN);
+        const bool isA = sr[i] < BM;
+        int64_t r = isA ? m0 + sr[i] : n0 + sr[i] - BM;
+        const int64_t n = isA ? p.M : p.N;
+        r = r < n ? r : n - 1;
+        sp[i] = (isA ? p.as : p.bs) + r * Ks;
+    }
+    ScaleRegs g[SR];
+    const auto load_g = [&](int st) {
+#pragma unroll
+        for (int i = 0; i < SR; ++i) g[i] = load_scales<TAIL>(sp[i] + 8 * (int64_t)st, Ks - 8 * (int64_t)st);
+    };
+    const auto settle = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < SR; ++i) store_scales(sX[buf], sr[i], g[i]);
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    const auto scales = [&](uint32_t (&va)[TM], uint32_t (&vb)[TN], int buf) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) va[i] = sX[buf][2 * (ra + 32 * i) + kh];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) vb[j] = sX[buf][2 * (BM + rb + 32 * j) + kh];
+    };
+
     f32x16 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -234,42 +286,19 @@ __global__ __launch_bounds__(kBlock) void mx4_tile_kernel(Mx4Args p, unsigned gm
         for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
-    const int stages = (int)((p.K + kTK - 1) / kTK);
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sC[0][0];
-    constexpr int SR = (BM + BN + kBlock - 1) / kBlock;  // scale rows per thread
-    ScaleRegs g[SR];
-    const auto issue = [&](int s, int buf) {
-        if (s >= stages) return;
-        stage_codes<BM>(p.a, m0, p.M, Kb, (int64_t)s * kRowBytes, lds0 + buf * kBytes, tid);
-        stage_codes<BN>(p.b, n0, p.N, Kb, (int64_t)s * kRowBytes, lds0 + buf * kBytes + BM * kRowBytes, tid);
-#pragma unroll
-        for (int i = 0; i < SR; ++i) {
-            const int r = tid + kBlock * i;
-            const bool isA = r < BM;
-            if (r < BM + BN)
-                g[i] = load_scales<TAIL>(isA ? p.as : p.bs, isA ? m0 + r : n0 + r - BM,
-                                         isA ? p.M : p.N, Ks, 8 * (int64_t)s);
-        }
-    };
-    const auto settle = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < SR; ++i) {
-            const int r = tid + kBlock * i;
-            if (r < BM + BN) store_scales(sX[buf], r, g[i]);
-        }
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    };
     Frags<TM, TN> f0, f1;
     uint32_t xa[TM], xb[TN], ya[TM], yb[TN];
-    issue(0, 0);
+    load_g(0);
+#pragma unroll
+    for (int i = 0; i < NA + NB; ++i) copy(0, 0, i);
     settle(0);
-    issue(1, 1);
-    const auto scales = [&](uint32_t (&va)[TM], uint32_t (&vb)[TN], int buf) {
+    // Stages past the last one repeat it and nothing uses them: the loop stays
+    // one block, which keeps the products between the copies (the compiler
+    // sinks them past a branch, and then nothing overlaps).
+    const auto clamped = [&](int st) { return st < stages ? st : stages - 1; };
+    load_g(clamped(1));
 #pragma unroll
-        for (int i = 0; i < TM; ++i) va[i] = sX[buf][2 * (ra + 32 * i) + kh];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) vb[j] = sX[buf][2 * (BM + rb + 32 * j) + kh];
-    };
+    for (int i = 0; i < NA + NB; ++i) copy(clamped(1), 1, i);
     scales(xa, xb, 0);
     read_frags<0, TAIL>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh, Ks - kh);
     for (int st = 0; st < stages; ++st) {
@@ -278,23 +307,38 @@ __global__ __launch_bounds__(kBlock) void mx4_tile_kernel(Mx4Args p, unsigned gm
         const uint8_t* cB = cA + BM * kRowBytes;
         const int64_t left = Ks - 8 * (int64_t)st - kh;  // blocks from this lane's first one on
         read_frags<1, TAIL>(f1, cA, cB, ra, rb, kh, left);
+        __builtin_amdgcn_sched_barrier(0);
         mma_step<0>(f0, xa, xb, acc);
+        __builtin_amdgcn_sched_barrier(0);
         read_frags<2, TAIL>(f0, cA, cB, ra, rb, kh, left);
+        __builtin_amdgcn_sched_barrier(0);
         mma_step<1>(f1, xa, xb, acc);
+        __builtin_amdgcn_sched_barrier(0);
         read_frags<3, TAIL>(f1, cA, cB, ra, rb, kh, left);
+        __builtin_amdgcn_sched_barrier(0);
         mma_step<2>(f0, xa, xb, acc);
+        __builtin_amdgcn_sched_barrier(0);
         settle(buf ^ 1);
         const uint8_t* nA = sC[buf ^ 1];
         scales(ya, yb, buf ^ 1);
         read_frags<0, TAIL>(f0, nA, nA + BM * kRowBytes, ra, rb, kh, left - 8);
-        issue(st + 2, buf);
-        mma_step<3>(f1, xa, xb, acc);
+        load_g(clamped(st + 2));
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int kPer = (NA + NB + TM * TN - 1) / (TM * TN);  // copies behind each product
+#pragma unroll
+        for (int q = 0; q < TM * TN; ++q) {
+            mma_one<3>(f1, xa, xb, acc, q / TN, q % TN);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = kPer * q; i < kPer * (q + 1) && i < NA + NB; ++i) copy(clamped(st + 2), buf, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i) xa[i] = ya[i];
 #pragma unroll
         for (int j = 0; j < TN; ++j) xb[j] = yb[j];
     }
-    // the last copies must have landed before the buffers hold the outputs
+    // every wave is done with the stage buffers before they hold the outputs
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     // D: column lane % 32, rows (v % 4) + 8 (v / 4) + 4 (lane / 32).  A strip of
     // 32 rows goes through the wave's own LDS to 8 columns per lane.
