@@ -83,69 +83,44 @@ MHC_DEV void finish8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 }
 
 // ---------------------------------------------------------------------------
-// Tiled product.  Workgroup: 4 waves as 2 x 2, each 32 TM x 32 TN outputs, K
-// in stages of 256 (128 bytes of codes and 8 scales per row).
+// Tiled product.  Workgroup: WM x WN waves, each 32 TM x 32 TN outputs, K in
+// stages of KS steps of 64 (KS = 4 or 2): 32 KS bytes of codes and 2 KS scale
+// bytes per row.
 //
-// LDS: a stage's rows of 128 bytes as 8 pieces of 16, piece c of row r at
-// place c ^ (r % 8), so that the 8 rows a read phase covers fall on different
-// banks.  Scales as two words per row, word h holding blocks h, 2 + h, 4 + h,
-// 6 + h: a lane (block half h) then has the scales of its 4 steps in one
-// register, and the instruction selects the byte.
+// LDS: NBUF stage buffers.  A row is 2 KS pieces of 16 bytes, piece c of row r
+// at place c ^ (r % 8) (KS = 2: c ^ (r / 2 % 4)), so that the 8 rows a read
+// phase covers fall on different banks.  Each 4 scale bytes of a row are one
+// word; a lane of block half h = lane / 32 shifts it by 8 h and finds the
+// scales of two steps in bytes 0 and 2, which the instruction selects.
 //
-// Pipeline: two LDS buffers and two register sets of fragments.  While step s
-// multiplies, step s + 1's fragments are read.  A stage's last fragments are
-// in registers before its last step, so the barrier that hands over the next
-// stage stands there: behind it the next stage's first fragments are read and
-// the copies of the stage after it start into the freed buffer, which gives
-// them a whole stage to land.
+// Pipeline: copies run NBUF - 1 stages ahead, straight from global memory to
+// LDS, and two register sets hold fragments: while one step multiplies, the
+// next one's are read.  A stage's last fragments are in registers before its
+// last step, so the one barrier per stage stands there: behind it the next
+// stage's first fragments are read and the copies of the stage NBUF ahead go
+// into the freed buffer, between that step's products.  The barrier waits for
+// the next stage's copies only (the counter retires in order).
 //
-// TAIL: K is no multiple of 256 (blocks past K are zeroed in A, and scale
-// rows, which then start at odd addresses, are read by bytes).
+// TAIL: K is no multiple of 64 KS.  Blocks past K are zeroed in A, and scale
+// rows, which then may start at odd addresses, go through registers byte by
+// byte.
 // ---------------------------------------------------------------------------
-constexpr int kTK = 256;
-constexpr int kRowBytes = kTK / 2;
-constexpr int kBlock = 256;
 
-// One copy of 16 bytes per lane from global memory straight to LDS: from a
-// wave-uniform base plus a lane offset to a wave-uniform LDS address plus 16
-// bytes per lane.  It is written as assembly because the compiler, which
-// cannot tell the two buffers apart, would wait for all copies before every
-// LDS read.  It has no register result; the wait is the vmcnt(0) before the
+// One copy of 16 (or 4) bytes per lane from global memory straight to LDS:
+// from a wave-uniform base plus a lane offset to a wave-uniform LDS address
+// plus 16 (4) bytes per lane.  It is written as assembly because the compiler,
+// which cannot tell the buffers apart, would wait for all copies before every
+// LDS read.  It has no register result; the wait is the vmcnt before the
 // barrier that hands the buffer over.
-MHC_DEV void copy_to_lds(const uint8_t* base, uint32_t off, uint32_t lds)
+MHC_DEV void copy16_to_lds(const uint8_t* base, uint32_t off, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
-
-struct ScaleRegs {
-    uint32_t lo, hi;
-};
-
-// the 8 scale bytes of one row's stage; `left` of them exist
-template <bool TAIL>
-MHC_DEV ScaleRegs load_scales(const uint8_t* p, int64_t left)
+MHC_DEV void copy4_to_lds(const uint8_t* base, uint32_t off, uint32_t lds)
 {
-    ScaleRegs r;
-    if (!TAIL) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        r.lo = v.x;
-        r.hi = v.y;
-    } else {
-        uint32_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 127u;
-        r.lo = v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24;
-        r.hi = v[4] | v[5] << 8 | v[6] << 16 | v[7] << 24;
-    }
-    return r;
-}
-
-MHC_DEV void store_scales(uint32_t* lds, int r, const ScaleRegs& s)
-{
-    // blocks 0 2 4 6 and 1 3 5 7
-    *reinterpret_cast<uint2*>(lds + 2 * r) =
-        make_uint2(mx_perm(s.hi, s.lo, 0x06040200u), mx_perm(s.hi, s.lo, 0x07050301u));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
 
 template <int TM, int TN>
@@ -153,50 +128,66 @@ struct Frags {
     uint4 a[TM], b[TN];
 };
 
-template <int S, bool TAIL, int TM, int TN>
+// place of piece c of row r
+template <int KS>
+MHC_DEV int piece_at(int r, int c)
+{
+    return KS == 4 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+}
+
+template <int KS, int S, bool TAIL, int TM, int TN>
 MHC_DEV void read_frags(Frags<TM, TN>& f, const uint8_t* sA, const uint8_t* sB, int ra, int rb,
                         int kh, int64_t left)
 {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int r = ra + 32 * i;
-        f.a[i] = *reinterpret_cast<const uint4*>(sA + r * kRowBytes + 16 * ((2 * S + kh) ^ (r & 7)));
+        f.a[i] = *reinterpret_cast<const uint4*>(sA + r * 32 * KS + 16 * piece_at<KS>(r, 2 * S + kh));
         if (TAIL && left <= 2 * S) f.a[i] = make_uint4(0, 0, 0, 0);  // a block past K
     }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
         const int r = rb + 32 * j;
-        f.b[j] = *reinterpret_cast<const uint4*>(sB + r * kRowBytes + 16 * ((2 * S + kh) ^ (r & 7)));
+        f.b[j] = *reinterpret_cast<const uint4*>(sB + r * 32 * KS + 16 * piece_at<KS>(r, 2 * S + kh));
     }
 }
 
-template <int S, int TM, int TN>
-MHC_DEV void mma_one(const Frags<TM, TN>& f, const uint32_t (&xa)[TM], const uint32_t (&xb)[TN],
-                     f32x16 (&acc)[TM][TN], int i, int j)
+// scale words of a stage: [word][tile], shifted for the lane's block half
+template <int KS, int TM, int TN>
+struct Scales {
+    uint32_t a[KS / 2][TM], b[KS / 2][TN];
+};
+
+template <int S, int KS, int TM, int TN>
+MHC_DEV void mma_one(const Frags<TM, TN>& f, const Scales<KS, TM, TN>& x, f32x16 (&acc)[TM][TN], int i,
+                     int j)
 {
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-        frag(f.a[i]), frag(f.b[j]), acc[i][j], kFp4, kFp4, S, (int)xa[i], S, (int)xb[j]);
+        frag(f.a[i]), frag(f.b[j]), acc[i][j], kFp4, kFp4, 2 * (S & 1), (int)x.a[S / 2][i], 2 * (S & 1),
+        (int)x.b[S / 2][j]);
 }
 
-template <int S, int TM, int TN>
-MHC_DEV void mma_step(const Frags<TM, TN>& f, const uint32_t (&xa)[TM], const uint32_t (&xb)[TN],
-                      f32x16 (&acc)[TM][TN])
+template <int S, int KS, int TM, int TN>
+MHC_DEV void mma_step(const Frags<TM, TN>& f, const Scales<KS, TM, TN>& x, f32x16 (&acc)[TM][TN])
 {
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) mma_one<S>(f, xa, xb, acc, i, j);
+    for (int q = 0; q < TM * TN; ++q) mma_one<S>(f, x, acc, q / TN, q % TN);
+    __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int TM, int TN, int EPI, bool TAIL>
-__global__ __launch_bounds__(kBlock) void mx4_tile_kernel(Mx4Args p, unsigned gm, unsigned gn)
+template <int TM, int TN, int WM, int WN, int KS, int NBUF, int EPI, bool TAIL>
+__global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsigned gm, unsigned gn)
 {
-    constexpr int BM = 64 * TM, BN = 64 * TN;
-    constexpr int kBytes = (BM + BN) * kRowBytes;  // codes of one stage
-    constexpr int kPitch = 32 * TN + 4;            // floats per staged output row
-    static_assert(4 * 32 * kPitch * 4 <= 2 * kBytes, "output strips fit the stage buffers");
-    __shared__ __attribute__((aligned(16))) uint8_t sC[2][kBytes];
-    __shared__ __attribute__((aligned(8))) uint32_t sX[2][2 * (BM + BN)];
+    constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, ROWS = BM + BN;
+    constexpr int kRowBytes = 32 * KS, kRowBlocks = 2 * KS, kWords = KS / 2;
+    constexpr int kBlock = 64 * WM * WN;
+    constexpr int kBytes = ROWS * kRowBytes;       // codes of one stage
+    constexpr int TS = TN < 2 ? TN : 2;            // tiles side by side in an output strip
+    constexpr int kPitch = 32 * TS + 4;            // floats per row of a strip
+    static_assert(WM * WN * 32 * kPitch * 4 <= NBUF * kBytes, "output strips fit the stage buffers");
+    __shared__ __attribute__((aligned(16))) uint8_t sC[NBUF][kBytes];
+    __shared__ uint32_t sX[NBUF][kWords][ROWS];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // Workgroups go to the 8 dies in turn; each die takes a run of
     // consecutive tiles, in bands of 4 tile rows, so that the rows and columns
@@ -214,70 +205,113 @@ __global__ __launch_bounds__(kBlock) void mx4_tile_kernel(Mx4Args p, unsigned gm
     }
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int64_t Kb = p.K / 2, Ks = p.K / 32;
-    const int ra = 32 * TM * (w & 1) + (lane & 31), rb = 32 * TN * (w >> 1) + (lane & 31);
+    const int wm = w % WM, wn = w / WM;
+    const int ra = 32 * TM * wm + (lane & 31), rb = 32 * TN * wn + (lane & 31);
     const int kh = lane >> 5;
-    const int stages = (int)((p.K + kTK - 1) / kTK);
+    const int stages = (int)((p.K + 64 * KS - 1) / (64 * KS));
 
-    // A thread copies piece c of rows 32 i + tid / 8 (its place in LDS is fixed
-    // by tid).  Rows past the matrix repeat its last one; their products are
-    // not used.  Row offsets fit 32 bits: 255 rows of at most 2^23 bytes.
-    constexpr int NA = 2 * TM, NB = 2 * TN;  // copies per thread and stage
-    const int c16 = 16 * ((tid & 7) ^ ((tid >> 3) & 7));
+    // A thread copies piece c of every kStep-th row from tid / (2 KS) on (c and
+    // its place in LDS are fixed by tid).  Rows past the matrix repeat its
+    // last one; their products are not used.  Row offsets fit 32 bits: 255
+    // rows of at most 2^23 bytes.
+    constexpr int kStep = kBlock / (2 * KS);
+    constexpr int NA = BM / kStep, NB = BN / kStep;     // code copies per thread and stage
+    constexpr int NX = (ROWS + kBlock - 1) / kBlock;    // scale copies
+    static_assert(BM % kStep == 0 && BN % kStep == 0 && kStep % 8 == 0, "whole copies, one swizzle per thread");
+    const int row0 = tid / (2 * KS), c16 = 16 * piece_at<KS>(row0, tid % (2 * KS));
     const uint8_t* baseA = p.a + m0 * Kb;
     const uint8_t* baseB = p.b + n0 * Kb;
     uint32_t offA[NA], offB[NB];
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-        const int64_t r = 32 * i + (tid >> 3), last = p.M - 1 - m0;
+        const int64_t r = kStep * i + row0, last = p.M - 1 - m0;
         offA[i] = (uint32_t)((r < last ? r : last) * Kb) + c16;
     }
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-        const int64_t r = 32 * i + (tid >> 3), last = p.N - 1 - n0;
+        const int64_t r = kStep * i + row0, last = p.N - 1 - n0;
         offB[i] = (uint32_t)((r < last ? r : last) * Kb) + c16;
     }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sC[0][0];
-    const auto copy = [&](int st, int buf, int i) {  // copy i of stage st
-        uint32_t cut = 0;
-        if (TAIL) {  // bytes past the row repeat its last piece
-            const int64_t over = (int64_t)st * kRowBytes + c16 - (Kb - 16);
-            cut = over > 0 ? (uint32_t)over : 0u;
-        }
-        const bool isA = i < NA;
-        const uint8_t* base = (isA ? baseA : baseB) + (int64_t)st * kRowBytes;
-        copy_to_lds(base, (isA ? offA[isA ? i : 0] : offB[isA ? 0 : i - NA]) - cut,
-                    lds0 + buf * kBytes + 16 * (kBlock * i + 64 * w));
-    };
-    // scale rows of this thread: row tid + 256 i of A's then B's (a workgroup
-    // with fewer rows than threads loads some twice)
-    constexpr int SR = (BM + BN + kBlock - 1) / kBlock;
-    const uint8_t* sp[SR];
-    int sr[SR];
+    // Scale words: a wave's 64 rows all belong to A or all to B (BM and BN are
+    // multiples of 64).  Where the rows are no multiple of the threads, some
+    // waves copy rows again that others copy too.
+    static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave's scale rows are one matrix's");
+    uint32_t offX[NX];
+    const uint8_t* baseX[NX];
+    int rowX[NX];
 #pragma unroll
-    for (int i = 0; i < SR; ++i) {
-        sr[i] = (tid + kBlock * i) % (BM + BN);
-        const bool isA = sr[i] < BM;
-        int64_t r = isA ? m0 + sr[i] : n0 + sr[i] - BM;
-        const int64_t n = isA ? p.M : p.N;
-        r = r < n ? r : n - 1;
-        sp[i] = (isA ? p.as : p.bs) + r * Ks;
+    for (int i = 0; i < NX; ++i) {
+        const int first = (64 * w + kBlock * i) % ROWS;  // wave-uniform
+        const bool isA = first < BM;
+        baseX[i] = isA ? p.as + m0 * Ks : p.bs + n0 * Ks;
+        const int64_t r = first - (isA ? 0 : BM) + lane, last = isA ? p.M - 1 - m0 : p.N - 1 - n0;
+        offX[i] = (uint32_t)((r < last ? r : last) * Ks);
+        rowX[i] = first;
     }
-    ScaleRegs g[SR];
-    const auto load_g = [&](int st) {
-#pragma unroll
-        for (int i = 0; i < SR; ++i) g[i] = load_scales<TAIL>(sp[i] + 8 * (int64_t)st, Ks - 8 * (int64_t)st);
+    const uint32_t ldsC = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sC[0][0];
+    const uint32_t ldsX = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint32_t*)&sX[0][0];
+    constexpr int NC = NA + NB + (TAIL ? 0 : kWords * NX);  // copies per thread and stage
+    const auto copy = [&](int st, int buf, int i) {  // copy i of stage st
+        if (i < NA + NB) {
+            uint32_t cut = 0;
+            if (TAIL) {  // bytes past the row repeat its last piece
+                const int64_t over = (int64_t)st * kRowBytes + c16 - (Kb - 16);
+                cut = over > 0 ? (uint32_t)over : 0u;
+            }
+            const bool isA = i < NA;
+            const uint8_t* base = (isA ? baseA : baseB) + (int64_t)st * kRowBytes;
+            copy16_to_lds(base, (isA ? offA[isA ? i : 0] : offB[isA ? 0 : i - NA]) - cut,
+                          ldsC + buf * kBytes + 16 * (kBlock * i + 64 * w));
+        } else {
+            const int x = (i - NA - NB) / kWords, q = (i - NA - NB) % kWords;
+            copy4_to_lds(baseX[x] + (int64_t)st * kRowBlocks + 4 * q, offX[x],
+                         ldsX + 4 * ((buf * kWords + q) * ROWS + rowX[x]));
+        }
     };
-    const auto settle = [&](int buf) {
+    const auto tail_scales = [&](int st, int buf) {
 #pragma unroll
-        for (int i = 0; i < SR; ++i) store_scales(sX[buf], sr[i], g[i]);
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        for (int i = 0; i < NX; ++i) {
+            const uint8_t* s = baseX[i] + offX[i] + (int64_t)st * kRowBlocks;
+#pragma unroll
+            for (int q = 0; q < kWords; ++q) {
+                uint32_t v = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v |= (uint32_t)((int64_t)st * kRowBlocks + 4 * q + k < Ks ? s[4 * q + k] : 127) << (8 * k);
+                sX[buf][q][rowX[i] + lane] = v;
+            }
+        }
     };
-    const auto scales = [&](uint32_t (&va)[TM], uint32_t (&vb)[TN], int buf) {
+    // Stages past the last one repeat it and nothing uses them: the loop stays
+    // one block, which keeps the products between the copies (the compiler
+    // sinks them past a branch, and then nothing overlaps).
+    const auto clamped = [&](int st) { return st < stages ? st : stages - 1; };
+    const auto scales = [&](Scales<KS, TM, TN>& x, int buf) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) va[i] = sX[buf][2 * (ra + 32 * i) + kh];
+        for (int q = 0; q < kWords; ++q) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) vb[j] = sX[buf][2 * (BM + rb + 32 * j) + kh];
+            for (int i = 0; i < TM; ++i) x.a[q][i] = sX[buf][q][ra + 32 * i];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) x.b[q][j] = sX[buf][q][BM + rb + 32 * j];
+        }
     };
+    const auto shifted = [&](Scales<KS, TM, TN>& x, const Scales<KS, TM, TN>& y) {
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) x.a[q][i] = y.a[q][i] >> (8 * kh);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) x.b[q][j] = y.b[q][j] >> (8 * kh);
+        }
+    };
+    // next stage's copies landed, everybody's reads of this one done
+    const auto hand_over = [&]() {
+        if (TAIL)
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"((NBUF - 2) * NC) : "memory");
+    };
+    static_assert((NBUF - 2) * NC < 64, "the copies in flight fit the counter");
 
     f32x16 acc[TM][TN];
 #pragma unroll
@@ -287,82 +321,78 @@ __global__ __launch_bounds__(kBlock) void mx4_tile_kernel(Mx4Args p, unsigned gm
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     Frags<TM, TN> f0, f1;
-    uint32_t xa[TM], xb[TN], ya[TM], yb[TN];
-    load_g(0);
+    Scales<KS, TM, TN> x, y;
 #pragma unroll
-    for (int i = 0; i < NA + NB; ++i) copy(0, 0, i);
-    settle(0);
-    // Stages past the last one repeat it and nothing uses them: the loop stays
-    // one block, which keeps the products between the copies (the compiler
-    // sinks them past a branch, and then nothing overlaps).
-    const auto clamped = [&](int st) { return st < stages ? st : stages - 1; };
-    load_g(clamped(1));
+    for (int b = 0; b < NBUF; ++b) {
+        if (b == NBUF - 1) hand_over();  // stage 0 (NBUF - 1 stages are on their way)
 #pragma unroll
-    for (int i = 0; i < NA + NB; ++i) copy(clamped(1), 1, i);
-    scales(xa, xb, 0);
-    read_frags<0, TAIL>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh, Ks - kh);
+        for (int i = 0; i < NC; ++i) copy(clamped(b), b, i);
+        if (TAIL) tail_scales(clamped(b), b);
+    }
+    if (TAIL) hand_over();
+    scales(y, 0);
+    shifted(x, y);
+    read_frags<KS, 0, TAIL>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh, Ks - kh);
+    int buf = 0;
     for (int st = 0; st < stages; ++st) {
-        const int buf = st & 1;
         const uint8_t* cA = sC[buf];
         const uint8_t* cB = cA + BM * kRowBytes;
-        const int64_t left = Ks - 8 * (int64_t)st - kh;  // blocks from this lane's first one on
-        read_frags<1, TAIL>(f1, cA, cB, ra, rb, kh, left);
+        const int nxt = buf + 1 < NBUF ? buf + 1 : 0;
+        const int64_t left = Ks - kRowBlocks * (int64_t)st - kh;  // blocks from this lane's first one on
+        read_frags<KS, 1, TAIL>(f1, cA, cB, ra, rb, kh, left);
+        mma_step<0>(f0, x, acc);
+        if constexpr (KS == 4) {
+            read_frags<KS, 2, TAIL>(f0, cA, cB, ra, rb, kh, left);
+            mma_step<1>(f1, x, acc);
+            read_frags<KS, 3, TAIL>(f1, cA, cB, ra, rb, kh, left);
+            mma_step<2>(f0, x, acc);
+        }
+        hand_over();
+        const uint8_t* nA = sC[nxt];
+        scales(y, nxt);
+        read_frags<KS, 0, TAIL>(f0, nA, nA + BM * kRowBytes, ra, rb, kh, left - kRowBlocks);
+        if (TAIL) tail_scales(clamped(st + NBUF), buf);
         __builtin_amdgcn_sched_barrier(0);
-        mma_step<0>(f0, xa, xb, acc);
-        __builtin_amdgcn_sched_barrier(0);
-        read_frags<2, TAIL>(f0, cA, cB, ra, rb, kh, left);
-        __builtin_amdgcn_sched_barrier(0);
-        mma_step<1>(f1, xa, xb, acc);
-        __builtin_amdgcn_sched_barrier(0);
-        read_frags<3, TAIL>(f1, cA, cB, ra, rb, kh, left);
-        __builtin_amdgcn_sched_barrier(0);
-        mma_step<2>(f0, xa, xb, acc);
-        __builtin_amdgcn_sched_barrier(0);
-        settle(buf ^ 1);
-        const uint8_t* nA = sC[buf ^ 1];
-        scales(ya, yb, buf ^ 1);
-        read_frags<0, TAIL>(f0, nA, nA + BM * kRowBytes, ra, rb, kh, left - 8);
-        load_g(clamped(st + 2));
-        __builtin_amdgcn_sched_barrier(0);
-        constexpr int kPer = (NA + NB + TM * TN - 1) / (TM * TN);  // copies behind each product
+        constexpr int kPer = (NC + TM * TN - 1) / (TM * TN);  // copies behind each product
 #pragma unroll
         for (int q = 0; q < TM * TN; ++q) {
-            mma_one<3>(f1, xa, xb, acc, q / TN, q % TN);
+            mma_one<KS - 1>(f1, x, acc, q / TN, q % TN);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = kPer * q; i < kPer * (q + 1) && i < NA + NB; ++i) copy(clamped(st + 2), buf, i);
+            for (int i = kPer * q; i < kPer * (q + 1) && i < NC; ++i) copy(clamped(st + NBUF), buf, i);
             __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int i = 0; i < TM; ++i) xa[i] = ya[i];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) xb[j] = yb[j];
+        shifted(x, y);
+        buf = nxt;
     }
     // every wave is done with the stage buffers before they hold the outputs
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    // D: column lane % 32, rows (v % 4) + 8 (v / 4) + 4 (lane / 32).  A strip of
-    // 32 rows goes through the wave's own LDS to 8 columns per lane.
+    // D: column lane % 32, rows (v % 4) + 8 (v / 4) + 4 (lane / 32).  Strips of
+    // 32 rows go through the wave's own LDS to 8 columns per lane.
     float* strip = reinterpret_cast<float*>(&sC[0][0]) + w * 32 * kPitch;
-    constexpr int kLanes = 4 * TN;                 // lanes per row
-    const int64_t mw = m0 + 32 * TM * (w & 1), nw = n0 + 32 * TN * (w >> 1);
+    constexpr int kLanes = 4 * TS;                 // lanes per row
+    const int64_t mw = m0 + 32 * TM * wm, nw = n0 + 32 * TN * wn;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        mhc_wave_lds_fence();  // the previous strip's reads come first
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+        for (int jj = 0; jj < TN; jj += TS) {
+            mhc_wave_lds_fence();  // the previous strip's reads come first
 #pragma unroll
-            for (int v = 0; v < 16; ++v)
-                strip[((v & 3) + 8 * (v >> 2) + 4 * kh) * kPitch + 32 * j + (lane & 31)] = acc[i][j][v];
-        mhc_wave_lds_fence();
+            for (int j = 0; j < TS; ++j)
 #pragma unroll
-        for (int q = 0; q < 32 * kLanes / 64; ++q) {
-            const int r = (64 / kLanes) * q + lane / kLanes, c = 8 * (lane % kLanes);
-            const int64_t m = mw + 32 * i + r, n = nw + c;
-            if (m < p.M && n < p.N) {
-                const float4 y0 = *reinterpret_cast<const float4*>(&strip[r * kPitch + c]);
-                const float4 y1 = *reinterpret_cast<const float4*>(&strip[r * kPitch + c + 4]);
-                const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-                finish8<EPI>(p, m, n, y);
+                for (int v = 0; v < 16; ++v)
+                    strip[((v & 3) + 8 * (v >> 2) + 4 * kh) * kPitch + 32 * j + (lane & 31)] = acc[i][jj + j][v];
+            mhc_wave_lds_fence();
+#pragma unroll
+            for (int q = 0; q < 32 * kLanes / 64; ++q) {
+                const int r = (64 / kLanes) * q + lane / kLanes, c = 8 * (lane % kLanes);
+                const int64_t m = mw + 32 * i + r, n = nw + 32 * jj + c;
+                if (m < p.M && n < p.N) {
+                    const float4 y0 = *reinterpret_cast<const float4*>(&strip[r * kPitch + c]);
+                    const float4 y1 = *reinterpret_cast<const float4*>(&strip[r * kPitch + c + 4]);
+                    const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                    finish8<EPI>(p, m, n, y);
+                }
             }
         }
     }
@@ -412,7 +442,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Args p)
         }
     };
     uint8_t* qx = sQ + p.M * Kb;
-    if (SRC == 0) {
+    if constexpr (SRC == 0) {
         load_b(0);
     } else {
         // quantise a: 8 columns per lane, a block per quad.  The first pieces
@@ -436,7 +466,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Args p)
             reinterpret_cast<uint32_t*>(sQ)[c] = code;
             if ((c & 3) == 0) qx[c >> 2] = (uint8_t)s;
         };
-        uint4 pre[kPre][SRC > 0 ? SRC : 1];
+        uint4 pre[kPre][SRC];
 #pragma unroll
         for (int i = 0; i < kPre; ++i) {
             int64_t c = tid + kThreads * i;
@@ -509,17 +539,18 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Args p)
     }
 }
 
-template <int TM, int TN, int EPI>
+template <int TM, int TN, int WM, int WN, int KS, int NBUF, int EPI>
 void tile_as(const Mx4Args& p, hipStream_t stream)
 {
-    const unsigned gm = (unsigned)((p.M + 64 * TM - 1) / (64 * TM));
-    const unsigned gn = (unsigned)((p.N + 64 * TN - 1) / (64 * TN));
-    if (p.K % kTK == 0)
-        hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, EPI, false>), dim3(gm * gn), dim3(kBlock), 0,
-                           stream, p, gm, gn);
+    constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
+    const unsigned gm = (unsigned)((p.M + BM - 1) / BM), gn = (unsigned)((p.N + BN - 1) / BN);
+    const dim3 block(64 * WM * WN);
+    if (p.K % (64 * KS) == 0)
+        hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, false>), dim3(gm * gn), block,
+                           0, stream, p, gm, gn);
     else
-        hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, EPI, true>), dim3(gm * gn), dim3(kBlock), 0,
-                           stream, p, gm, gn);
+        hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, true>), dim3(gm * gn), block,
+                           0, stream, p, gm, gn);
 }
 
 template <int MT, int SRC, int EPI>
@@ -548,11 +579,11 @@ hipError_t matmul_as(const Mx4Args& p, int src, hipStream_t stream)
         const int64_t t256 = ((p.M + 255) / 256) * ((p.N + 255) / 256);
         const int64_t t128 = ((p.M + 127) / 128) * ((p.N + 127) / 128);
         if (t256 >= 256)
-            tile_as<4, 4, EPI>(p, stream);
+            tile_as<4, 4, 2, 2, 4, 2, EPI>(p, stream);
         else if (t128 >= 256)
-            tile_as<2, 2, EPI>(p, stream);
+            tile_as<2, 2, 2, 2, 4, 2, EPI>(p, stream);
         else
-            tile_as<1, 1, EPI>(p, stream);
+            tile_as<1, 1, 2, 2, 4, 2, EPI>(p, stream);
     }
     return hipGetLastError();
 }
