@@ -101,9 +101,10 @@ MHC_DEV void finish8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 // into the freed buffer, between that step's products.  The barrier waits for
 // the next stage's copies only (the counter retires in order).
 //
-// TAIL: K is no multiple of 64 KS.  Blocks past K are zeroed in A, and scale
-// rows, which then may start at odd addresses, go through registers byte by
-// byte.
+// TAIL: K is no multiple of 64 KS.  Blocks past K are zeroed in A and get a
+// scale of 1.  Rows of scales may then start at any byte: the aligned words
+// around a row's bytes are copied, one more than it has, and a lane shifts its
+// bytes out of two of them.
 // ---------------------------------------------------------------------------
 
 // One copy of 16 (or 4) bytes per lane from global memory straight to LDS:
@@ -152,14 +153,14 @@ MHC_DEV void read_frags(Frags<TM, TN>& f, const uint8_t* sA, const uint8_t* sB, 
     }
 }
 
-// scale words of a stage: [word][tile], shifted for the lane's block half
-template <int KS, int TM, int TN>
+// scale words of a stage: [word][tile]
+template <int W, int TM, int TN>
 struct Scales {
-    uint32_t a[KS / 2][TM], b[KS / 2][TN];
+    uint32_t a[W][TM], b[W][TN];
 };
 
-template <int S, int KS, int TM, int TN>
-MHC_DEV void mma_one(const Frags<TM, TN>& f, const Scales<KS, TM, TN>& x, f32x16 (&acc)[TM][TN], int i,
+template <int S, int W, int TM, int TN>
+MHC_DEV void mma_one(const Frags<TM, TN>& f, const Scales<W, TM, TN>& x, f32x16 (&acc)[TM][TN], int i,
                      int j)
 {
     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
@@ -167,8 +168,8 @@ MHC_DEV void mma_one(const Frags<TM, TN>& f, const Scales<KS, TM, TN>& x, f32x16
         (int)x.b[S / 2][j]);
 }
 
-template <int S, int KS, int TM, int TN>
-MHC_DEV void mma_step(const Frags<TM, TN>& f, const Scales<KS, TM, TN>& x, f32x16 (&acc)[TM][TN])
+template <int S, int W, int TM, int TN>
+MHC_DEV void mma_step(const Frags<TM, TN>& f, const Scales<W, TM, TN>& x, f32x16 (&acc)[TM][TN])
 {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -180,14 +181,15 @@ template <int TM, int TN, int WM, int WN, int KS, int NBUF, int EPI, bool TAIL>
 __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsigned gm, unsigned gn)
 {
     constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, ROWS = BM + BN;
-    constexpr int kRowBytes = 32 * KS, kRowBlocks = 2 * KS, kWords = KS / 2;
+    constexpr int kRowBytes = 32 * KS, kRowBlocks = 2 * KS;
+    constexpr int kWords = KS / 2, kCopied = TAIL ? kWords + 1 : kWords;  // scale words of a row
     constexpr int kBlock = 64 * WM * WN;
     constexpr int kBytes = ROWS * kRowBytes;       // codes of one stage
     constexpr int TS = TN < 2 ? TN : 2;            // tiles side by side in an output strip
     constexpr int kPitch = 32 * TS + 4;            // floats per row of a strip
     static_assert(WM * WN * 32 * kPitch * 4 <= NBUF * kBytes, "output strips fit the stage buffers");
     __shared__ __attribute__((aligned(16))) uint8_t sC[NBUF][kBytes];
-    __shared__ uint32_t sX[NBUF][kWords][ROWS];
+    __shared__ uint32_t sX[NBUF][kCopied][ROWS];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // Workgroups go to the 8 dies in turn; each die takes a run of
     // consecutive tiles, in bands of 4 tile rows, so that the rows and columns
@@ -236,21 +238,28 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
     // multiples of 64).  Where the rows are no multiple of the threads, some
     // waves copy rows again that others copy too.
     static_assert(BM % 64 == 0 && BN % 64 == 0, "a wave's scale rows are one matrix's");
-    uint32_t offX[NX];
+    uint32_t offX[NX], endX[NX];  // endX: offset of the matrix's last word of scales
     const uint8_t* baseX[NX];
     int rowX[NX];
 #pragma unroll
     for (int i = 0; i < NX; ++i) {
         const int first = (64 * w + kBlock * i) % ROWS;  // wave-uniform
         const bool isA = first < BM;
-        baseX[i] = isA ? p.as + m0 * Ks : p.bs + n0 * Ks;
-        const int64_t r = first - (isA ? 0 : BM) + lane, last = isA ? p.M - 1 - m0 : p.N - 1 - n0;
-        offX[i] = (uint32_t)((r < last ? r : last) * Ks);
+        const int64_t b0 = isA ? m0 : n0, n = isA ? p.M : p.N, base = (b0 * Ks) & ~(int64_t)3;
+        const int64_t r = b0 + first - (isA ? 0 : BM) + lane;
+        baseX[i] = (isA ? p.as : p.bs) + base;
+        offX[i] = (uint32_t)((((r < n ? r : n - 1) * Ks) & ~(int64_t)3) - base);
+        const int64_t end = ((n * Ks - 1) & ~(int64_t)3) - base;
+        endX[i] = (uint32_t)(end < 0xffffffff ? end : 0xffffffff);
         rowX[i] = first;
     }
+    // byte of its first word where a lane's scales begin (the same for all its
+    // rows: they are 32 apart), plus its block half
+    const int sa = (TAIL ? (int)(((m0 + ra) * Ks) & 3) : 0) + kh;
+    const int sb = (TAIL ? (int)(((n0 + rb) * Ks) & 3) : 0) + kh;
     const uint32_t ldsC = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sC[0][0];
     const uint32_t ldsX = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint32_t*)&sX[0][0];
-    constexpr int NC = NA + NB + (TAIL ? 0 : kWords * NX);  // copies per thread and stage
+    constexpr int NC = NA + NB + kCopied * NX;      // copies per thread and stage
     const auto copy = [&](int st, int buf, int i) {  // copy i of stage st
         if (i < NA + NB) {
             uint32_t cut = 0;
@@ -263,53 +272,47 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
             copy16_to_lds(base, (isA ? offA[isA ? i : 0] : offB[isA ? 0 : i - NA]) - cut,
                           ldsC + buf * kBytes + 16 * (kBlock * i + 64 * w));
         } else {
-            const int x = (i - NA - NB) / kWords, q = (i - NA - NB) % kWords;
-            copy4_to_lds(baseX[x] + (int64_t)st * kRowBlocks + 4 * q, offX[x],
-                         ldsX + 4 * ((buf * kWords + q) * ROWS + rowX[x]));
-        }
-    };
-    const auto tail_scales = [&](int st, int buf) {
-#pragma unroll
-        for (int i = 0; i < NX; ++i) {
-            const uint8_t* s = baseX[i] + offX[i] + (int64_t)st * kRowBlocks;
-#pragma unroll
-            for (int q = 0; q < kWords; ++q) {
-                uint32_t v = 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v |= (uint32_t)((int64_t)st * kRowBlocks + 4 * q + k < Ks ? s[4 * q + k] : 127) << (8 * k);
-                sX[buf][q][rowX[i] + lane] = v;
-            }
+            const int x = (i - NA - NB) / kCopied, q = (i - NA - NB) % kCopied;
+            const uint32_t at = (uint32_t)st * kRowBlocks + 4 * q;  // at most 2^19
+            uint32_t off = offX[x] + at;
+            if (TAIL) off = off < endX[x] ? off : endX[x];  // a word past the last: not used
+            copy4_to_lds(baseX[x], off, ldsX + 4 * ((buf * kCopied + q) * ROWS + rowX[x]));
         }
     };
     // Stages past the last one repeat it and nothing uses them: the loop stays
     // one block, which keeps the products between the copies (the compiler
     // sinks them past a branch, and then nothing overlaps).
     const auto clamped = [&](int st) { return st < stages ? st : stages - 1; };
-    const auto scales = [&](Scales<KS, TM, TN>& x, int buf) {
+    const auto scales = [&](Scales<kCopied, TM, TN>& y, int buf) {
 #pragma unroll
-        for (int q = 0; q < kWords; ++q) {
+        for (int q = 0; q < kCopied; ++q) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) x.a[q][i] = sX[buf][q][ra + 32 * i];
+            for (int i = 0; i < TM; ++i) y.a[q][i] = sX[buf][q][ra + 32 * i];
 #pragma unroll
-            for (int j = 0; j < TN; ++j) x.b[q][j] = sX[buf][q][BM + rb + 32 * j];
+            for (int j = 0; j < TN; ++j) y.b[q][j] = sX[buf][q][BM + rb + 32 * j];
         }
     };
-    const auto shifted = [&](Scales<KS, TM, TN>& x, const Scales<KS, TM, TN>& y) {
+    // the lane's own scales in bytes 0 and 2; `left` blocks exist
+    const auto shifted = [&](Scales<kWords, TM, TN>& x, const Scales<kCopied, TM, TN>& y, int64_t left) {
+        const auto pick = [&](uint32_t lo, uint32_t hi, int s, int q) {
+            if (!TAIL) return lo >> (8 * s);
+            uint32_t v = (uint32_t)((((uint64_t)hi << 32) | lo) >> (8 * s));
+            if (left <= 4 * q) v = 0x007f007fu;
+            else if (left <= 4 * q + 2) v = (v & 0xffu) | 0x007f0000u;
+            return v;
+        };
 #pragma unroll
         for (int q = 0; q < kWords; ++q) {
+            constexpr int one = TAIL ? 1 : 0;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) x.a[q][i] = y.a[q][i] >> (8 * kh);
+            for (int i = 0; i < TM; ++i) x.a[q][i] = pick(y.a[q][i], y.a[q + one][i], sa, q);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) x.b[q][j] = y.b[q][j] >> (8 * kh);
+            for (int j = 0; j < TN; ++j) x.b[q][j] = pick(y.b[q][j], y.b[q + one][j], sb, q);
         }
     };
     // next stage's copies landed, everybody's reads of this one done
     const auto hand_over = [&]() {
-        if (TAIL)
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        else
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"((NBUF - 2) * NC) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"((NBUF - 2) * NC) : "memory");
     };
     static_assert((NBUF - 2) * NC < 64, "the copies in flight fit the counter");
 
@@ -321,17 +324,16 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
     Frags<TM, TN> f0, f1;
-    Scales<KS, TM, TN> x, y;
+    Scales<kWords, TM, TN> x;
+    Scales<kCopied, TM, TN> y;
 #pragma unroll
     for (int b = 0; b < NBUF; ++b) {
         if (b == NBUF - 1) hand_over();  // stage 0 (NBUF - 1 stages are on their way)
 #pragma unroll
         for (int i = 0; i < NC; ++i) copy(clamped(b), b, i);
-        if (TAIL) tail_scales(clamped(b), b);
     }
-    if (TAIL) hand_over();
     scales(y, 0);
-    shifted(x, y);
+    shifted(x, y, Ks - kh);
     read_frags<KS, 0, TAIL>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh, Ks - kh);
     int buf = 0;
     for (int st = 0; st < stages; ++st) {
@@ -351,7 +353,6 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
         const uint8_t* nA = sC[nxt];
         scales(y, nxt);
         read_frags<KS, 0, TAIL>(f0, nA, nA + BM * kRowBytes, ra, rb, kh, left - kRowBlocks);
-        if (TAIL) tail_scales(clamped(st + NBUF), buf);
         __builtin_amdgcn_sched_barrier(0);
         constexpr int kPer = (NC + TM * TN - 1) / (TM * TN);  // copies behind each product
 #pragma unroll
@@ -362,7 +363,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
             for (int i = kPer * q; i < kPer * (q + 1) && i < NC; ++i) copy(clamped(st + NBUF), buf, i);
             __builtin_amdgcn_sched_barrier(0);
         }
-        shifted(x, y);
+        shifted(x, y, left - kRowBlocks);
         buf = nxt;
     }
     // every wave is done with the stage buffers before they hold the outputs
@@ -399,131 +400,174 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
 }
 
 // ---------------------------------------------------------------------------
-// Few rows of a (up to 16 MT): bound by reading b once.  A workgroup takes 16
-// rows of b and all of a; its 8 waves split K, and within a wave the lane
-// quarters (l / 16) split it again: each lane reads a run of consecutive
-// blocks of its row.  A sum may take the blocks in any order, so both operands
-// only have to agree, and the 16 x 16 x 128 instruction multiplies 4 blocks
-// that are not neighbours.  All of a wave's loads of b are issued at once.
-// The waves' partial sums meet in LDS and are added in wave order.
+// Few rows of a (up to 16): bound by reading b once.  A workgroup takes 16
+// rows of b and all of a, K in panels of up to PT tiles of 256.  Waves 4..7
+// copy the panel of b to LDS, every instruction 8 whole lines of 128 bytes;
+// meanwhile waves 0..3 put a there.  Then the 8 waves share the tiles; their
+// partial sums meet in LDS at the end and are added in wave order.
 //
-// SRC 0: a is packed.  SRC 1, 2 (MT = 1): a is bf16 or fp32 and every
-// workgroup quantises it for itself into LDS, while its loads of b are in
-// flight: one launch instead of two, for a call that lasts a few microseconds.
+// Whole lines are the point: loading b in the layout the instruction wants (16
+// bytes of 64 different lines at a time) ran at a third of this speed.
+//
+// SRC 0: a is packed and copied like b.  SRC 1, 2: a is bf16 or fp32, and every
+// workgroup quantises it for itself while its copies of b are under way: one
+// launch instead of two, for a call that lasts a few microseconds.
+//
+// LDS per tile: 16 rows of b, then MR rows of a (MR: M rounded up to a power of
+// two), each 128 bytes with piece c of row r at place c ^ (r % 8); then 8 scale
+// bytes of each row.  Lanes of rows past M use row M - 1; only their own
+// columns of the result, which are dropped, depend on them.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
-constexpr int kFewRun = 8;  // blocks per lane and pass
+constexpr int kFewThreads = 64 * kFewWaves;
 
-template <int MT, int SRC, int EPI>
-__global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Args p)
+struct FewShape {
+    int MR, LR, PT;      // rows of a in LDS and their logarithm, tiles per panel
+    unsigned lds;        // bytes
+};
+
+__host__ __device__ constexpr int few_tile_bytes(int MR) { return (16 + MR) * 136; }
+
+template <int SRC, int EPI>
+__global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShape sh)
 {
-    extern __shared__ __attribute__((aligned(16))) uint8_t sQ[];  // SRC > 0: codes, then scales
-    __shared__ float sR[kFewWaves][MT][16][17];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
+    __shared__ float sR[kFewWaves][16][17];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row = lane & 15, kq = lane >> 4;
+    const int M = (int)p.M, MR = sh.MR, PT = sh.PT;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     const int64_t Ks = p.K / 32, Kb = p.K / 2;
-    const int64_t per = (Ks + 4 * kFewWaves - 1) / (4 * kFewWaves);
-    const int64_t first = (4 * w + kq) * per;  // this lane's run of blocks
-    int64_t n = n0 + row;
-    n = n < p.N ? n : p.N - 1;
-    const uint8_t* bc = p.b + n * Kb;
-    const uint8_t* bx = p.bs + n * Ks;
-    uint4 fb[kFewRun];
-    uint32_t xb[kFewRun];
-    const auto load_b = [&](int64_t at) {
-#pragma unroll
-        for (int s = 0; s < kFewRun; ++s) {
-            int64_t k = first + at + s;
-            k = k < Ks ? k : Ks - 1;
-            const mhc_u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const mhc_u32x4*>(bc + 16 * k));
-            fb[s] = make_uint4(v.x, v.y, v.z, v.w);
-            xb[s] = bx[k];
+    const int tiles = (int)((p.K + 255) / 256);
+    const bool words = (Ks & 3) == 0;  // scale rows are whole words
+    uint8_t* sB = sm;                                  // [PT][16][128]
+    uint8_t* sA = sB + (int64_t)PT * 16 * 128;         // [PT][MR][128]
+    uint8_t* xB = sA + (int64_t)PT * MR * 128;         // [PT][16][8]
+    uint8_t* xA = xB + PT * 16 * 8;                    // [PT][MR][8]
+    const auto lds_at = [](const void* q) {
+        return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)q);
+    };
+    const int nB = (int)(p.N - n0 < 16 ? p.N - n0 : 16);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    const int ma = row < M ? row : M - 1;
+
+    // codes of 2^lr rows (`have` exist) of a panel to LDS: 4 waves, 8 rows of
+    // 128 bytes per instruction (lanes past the end are switched off)
+    const auto copy_codes = [&](const uint8_t* src, int lr, int have, int t0, int nt, uint8_t* dst, int wv) {
+        const uint32_t l0 = lds_at(dst);
+        const int pieces = (nt << lr) * 8;
+        for (int q = 64 * wv; q < pieces; q += 256) {
+            const int e = q + lane;
+            if (e < pieces) {
+                const int r = (e >> 3) & ((1 << lr) - 1), t = e >> (3 + lr), c = (e & 7) ^ (r & 7);
+                int64_t kb = (int64_t)(t0 + t) * 128 + 16 * c;
+                kb = kb < Kb ? kb : Kb - 16;  // bytes past the row: not used
+                const int64_t rr = r < have ? r : have - 1;
+                copy16_to_lds(src, (uint32_t)(rr * Kb + kb), l0 + 16 * q);
+            }
         }
     };
-    uint8_t* qx = sQ + p.M * Kb;
-    if constexpr (SRC == 0) {
-        load_b(0);
-    } else {
-        // quantise a: 8 columns per lane, a block per quad.  The first pieces
-        // are loaded before b, since loads complete in order.
-        constexpr int kPre = 2, kThreads = 64 * kFewWaves;
-        const int64_t chunks = p.M * (p.K / 8);
-        const uint4* av = reinterpret_cast<const uint4*>(p.a);
-        const auto quantise = [&](int64_t c, uint4 q, uint4 q2) {
-            uint32_t code, s;
-            if (SRC == 1) {
-                const uint32_t amax = mx_quad_max(mx_amax8(q));
-                s = mx_scale_byte<kE2M1>(amax);
-                code = mx_encode8_e2m1(q, amax, s);
-            } else {
-                const float4 u = __builtin_bit_cast(float4, q), v = __builtin_bit_cast(float4, q2);
-                float f[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-                const uint32_t amax = mx_quad_max(mx_amax8(f));
-                s = mx_scale_byte<kE2M1>(amax);
-                code = mx_encode8_e2m1(f, amax, s);
-            }
-            reinterpret_cast<uint32_t*>(sQ)[c] = code;
-            if ((c & 3) == 0) qx[c >> 2] = (uint8_t)s;
-        };
-        uint4 pre[kPre][SRC];
+    const auto copy_scales = [&](const uint8_t* src, int lr, int have, int t0, int nt, uint8_t* dst, int wv) {
+        const uint32_t l0 = lds_at(dst);
+        const int n = (nt << lr) * 2;
+        for (int q = 64 * wv; q < n; q += 256) {
+            const int e = q + lane;
+            if (e < n) {
+                const int r = (e >> 1) & ((1 << lr) - 1), t = e >> (1 + lr);
+                int64_t ks = (int64_t)(t0 + t) * 8 + 4 * (e & 1);
+                const int64_t rr = r < have ? r : have - 1;
+                if (words) {
+                    ks = ks < Ks ? ks : Ks - 4;
+                    copy4_to_lds(src, (uint32_t)(rr * Ks + ks), l0 + 4 * q);
+                } else {
+                    uint32_t v = 0;
 #pragma unroll
-        for (int i = 0; i < kPre; ++i) {
-            int64_t c = tid + kThreads * i;
-            c = c < chunks ? c : chunks - 1;
-#pragma unroll
-            for (int h = 0; h < SRC; ++h) pre[i][h] = av[SRC * c + h];
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        load_b(0);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < kPre; ++i)
-            if (tid + kThreads * i < chunks) quantise(tid + kThreads * i, pre[i][0], pre[i][SRC - 1]);
-        for (int64_t c = tid + kThreads * kPre; c < chunks; c += kThreads)
-            quantise(c, av[SRC * c], av[SRC * c + SRC - 1]);
-        mhc_lds_barrier();
-    }
-    f32x4 acc[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int64_t at = 0;;) {
-#pragma unroll
-        for (int s = 0; s < kFewRun; ++s) {
-            const int64_t k = first + at + s;
-            const bool live = at + s < per && k < Ks;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const int64_t m = 16 * t + row;
-                uint4 fa = make_uint4(0, 0, 0, 0);
-                uint32_t xa = 127;
-                if (live && m < p.M) {
-                    if (SRC > 0) {
-                        fa = *reinterpret_cast<const uint4*>(sQ + m * Kb + 16 * k);
-                        xa = qx[m * Ks + k];
-                    } else {
-                        fa = *reinterpret_cast<const uint4*>(p.a + m * Kb + 16 * k);
-                        xa = p.as[m * Ks + k];
-                    }
+                    for (int k = 0; k < 4; ++k) v |= (uint32_t)(ks + k < Ks ? src[rr * Ks + ks + k] : 127) << (8 * k);
+                    reinterpret_cast<uint32_t*>(dst)[e] = v;
                 }
-                // a dead block is zero in a, and its (repeated) scale of b is
-                // replaced, so that a NaN there stays out
-                acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    frag(fb[s]), frag(fa), acc[t], kFp4, kFp4, 0, live ? (int)xb[s] : 127, 0, (int)xa);
             }
         }
-        at += kFewRun;
-        if (at >= per) break;
-        load_b(at);
+    };
+
+    for (int t0 = 0; t0 < tiles; t0 += PT) {
+        const int nt = tiles - t0 < PT ? tiles - t0 : PT;
+        if (t0 > 0) {  // everybody is done with the panel before
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        if (w >= 4) {
+            copy_codes(p.b + n0 * Kb, 4, nB, t0, nt, sB, w - 4);
+            copy_scales(p.bs + n0 * Ks, 4, nB, t0, nt, xB, w - 4);
+        } else if constexpr (SRC == 0) {
+            copy_codes(p.a, sh.LR, M, t0, nt, sA, w);
+            copy_scales(p.as, sh.LR, M, t0, nt, xA, w);
+        } else {
+            // quantise a: 8 columns per lane, a block per quad
+            const uint4* av = reinterpret_cast<const uint4*>(p.a);
+            const int C8 = (int)(p.K / 8), c0 = t0 * 32;
+            const int nc = C8 - c0 < nt * 32 ? C8 - c0 : nt * 32;  // chunks per row
+            // 4 chunks' loads at once; both counts are multiples of 4, so a
+            // quad of lanes is whole
+            const int total = M * nc;
+            for (int j = tid; j < total; j += 1024) {
+                uint4 v[4][SRC];
+                int mi[4], ii[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int e = j + 256 * u < total ? j + 256 * u : total - 1;
+                    mi[u] = e / nc;
+                    ii[u] = e - mi[u] * nc;
+                    const int64_t g = (int64_t)mi[u] * C8 + c0 + ii[u];
+#pragma unroll
+                    for (int h = 0; h < SRC; ++h) v[u][h] = av[SRC * g + h];
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (j + 256 * u >= total) break;
+                    uint32_t code, s;
+                    if constexpr (SRC == 1) {
+                        const uint32_t amax = mx_quad_max(mx_amax8(v[u][0]));
+                        s = mx_scale_byte<kE2M1>(amax);
+                        code = mx_encode8_e2m1(v[u][0], amax, s);
+                    } else {
+                        const float4 x0 = __builtin_bit_cast(float4, v[u][0]);
+                        const float4 x1 = __builtin_bit_cast(float4, v[u][SRC - 1]);
+                        float f[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                        const uint32_t amax = mx_quad_max(mx_amax8(f));
+                        s = mx_scale_byte<kE2M1>(amax);
+                        code = mx_encode8_e2m1(f, amax, s);
+                    }
+                    const int k = ii[u] >> 2, at = (k >> 3) * MR + mi[u];
+                    *reinterpret_cast<uint32_t*>(sA + at * 128 + 16 * ((k & 7) ^ (mi[u] & 7)) + 4 * (ii[u] & 3)) = code;
+                    if ((ii[u] & 3) == 0) xA[at * 8 + (k & 7)] = (uint8_t)s;
+                }
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        for (int t = w; t < nt; t += kFewWaves) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int64_t k = (int64_t)(t0 + t) * 8 + 4 * s + kq;  // this lane's block
+                const bool live = k < Ks;
+                uint4 fb = *reinterpret_cast<const uint4*>(sB + (t * 16 + row) * 128 + 16 * ((4 * s + kq) ^ (row & 7)));
+                uint4 fa = *reinterpret_cast<const uint4*>(sA + (t * MR + ma) * 128 + 16 * ((4 * s + kq) ^ (ma & 7)));
+                uint32_t xb = *reinterpret_cast<const uint32_t*>(xB + (t * 16 + row) * 8 + 4 * s) >> (8 * kq);
+                uint32_t xa = *reinterpret_cast<const uint32_t*>(xA + (t * MR + ma) * 8 + 4 * s) >> (8 * kq);
+                if (!live) {  // a block past K
+                    fa = make_uint4(0, 0, 0, 0);
+                    fb = fa;
+                    xa = xb = 127;
+                }
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(fb), frag(fa), acc, kFp4, kFp4, 0,
+                                                                       (int)xb, 0, (int)xa);
+            }
+        }
     }
     // D: row (of b) 4 (lane / 16) + v, column (row of a) lane % 16
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) sR[w][t][row][4 * kq + v] = acc[t][v];
+    for (int v = 0; v < 4; ++v) sR[w][row][4 * kq + v] = acc[v];
     __syncthreads();
     // 8 columns per thread: 2 threads per row of a
-    if (tid < 32 * MT) {
+    if (tid < 32) {
         const int64_t m = tid >> 1, nn = n0 + 8 * (tid & 1);
         if (m < p.M && nn < p.N) {
             float y[8];
@@ -531,7 +575,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void mx4_few_kernel(Mx4Args p)
             for (int e = 0; e < 8; ++e) {
                 float s = 0.f;
 #pragma unroll
-                for (int ww = 0; ww < kFewWaves; ++ww) s += sR[ww][tid >> 5][(tid >> 1) & 15][8 * (tid & 1) + e];
+                for (int ww = 0; ww < kFewWaves; ++ww) s += sR[ww][tid >> 1][8 * (tid & 1) + e];
                 y[e] = s;
             }
             finish8<EPI>(p, m, nn, y);
@@ -548,42 +592,63 @@ void tile_as(const Mx4Args& p, hipStream_t stream)
     if (p.K % (64 * KS) == 0)
         hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, false>), dim3(gm * gn), block,
                            0, stream, p, gm, gn);
-    else
+    else if constexpr (WM * WN < 8)
         hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, true>), dim3(gm * gn), block,
                            0, stream, p, gm, gn);
 }
 
-template <int MT, int SRC, int EPI>
+// Panels sized for two workgroups per compute unit.
+FewShape few_shape(int64_t M, int64_t K)
+{
+    FewShape s{1, 0, 0, 0};
+    for (; s.MR < M; s.MR *= 2) ++s.LR;
+    const int64_t tiles = (K + 255) / 256, most = 70 * 1024 / few_tile_bytes(s.MR);
+    const int64_t panels = (tiles + most - 1) / most;
+    s.PT = (int)((tiles + panels - 1) / panels);
+    s.lds = (unsigned)(s.PT * few_tile_bytes(s.MR));
+    return s;
+}
+
+template <int SRC, int EPI>
 void few_as(const Mx4Args& p, hipStream_t stream)
 {
-    const unsigned lds = SRC > 0 ? (unsigned)(p.M * (p.K / 2 + p.K / 32)) : 0u;
-    hipLaunchKernelGGL((mx4_few_kernel<MT, SRC, EPI>), dim3((unsigned)((p.N + 15) / 16)),
-                       dim3(64 * kFewWaves), lds, stream, p);
+    const FewShape sh = few_shape(p.M, p.K);
+    hipLaunchKernelGGL((mx4_few_kernel<SRC, EPI>), dim3((unsigned)((p.N + 15) / 16)), dim3(kFewThreads),
+                       sh.lds, stream, p, sh);
 }
 
 template <int EPI>
 hipError_t matmul_as(const Mx4Args& p, int src, hipStream_t stream)
 {
     if (src == 1) {
-        few_as<1, 1, EPI>(p, stream);
+        few_as<1, EPI>(p, stream);
     } else if (src == 2) {
-        few_as<1, 2, EPI>(p, stream);
+        few_as<2, EPI>(p, stream);
     } else if (p.M <= 16) {
-        few_as<1, 0, EPI>(p, stream);
-    } else if (p.M <= 32) {
-        few_as<2, 0, EPI>(p, stream);
-    } else if (p.M <= 64) {
-        few_as<4, 0, EPI>(p, stream);
+        few_as<0, EPI>(p, stream);
     } else {
-        // the largest tile that still gives every compute unit one
+        // Large tiles move the fewest operand bytes per product and win as
+        // soon as they cover most of the chip; below that, more tiles.
+        // Measured (us, K = 4096 unless named): 4096 x 4096 (256 tiles of 256)
+        // 45 against 59 with tiles of 128; 2048 x 2048 (64, 256) 29 / 17, 35 with
+        // tiles of 64; 512 x 7168, K = 7168 (56, 224) 55 / 26 / 52; 256 x 4096
+        // (16, 64) 27 / 13 / 9.  Three stage buffers instead of two pay while a
+        // compute unit has one tile (2048 x 2048: 17.3 / 18.8), cost the second
+        // workgroup otherwise (4096 x 4096: 65 / 59).
         const int64_t t256 = ((p.M + 255) / 256) * ((p.N + 255) / 256);
         const int64_t t128 = ((p.M + 127) / 128) * ((p.N + 127) / 128);
-        if (t256 >= 256)
+        // (8 waves are 3 % faster than 4 on the large tile, but with the tail's
+        // shifts they spill)
+        if (t256 >= 192 && p.K % 256 == 0)
+            tile_as<2, 4, 4, 2, 4, 2, EPI>(p, stream);
+        else if (t256 >= 192)
             tile_as<4, 4, 2, 2, 4, 2, EPI>(p, stream);
-        else if (t128 >= 256)
+        else if (t128 > 256)
             tile_as<2, 2, 2, 2, 4, 2, EPI>(p, stream);
+        else if (t128 >= 128)
+            tile_as<2, 2, 2, 2, 4, 3, EPI>(p, stream);
         else
-            tile_as<1, 1, 2, 2, 4, 2, EPI>(p, stream);
+            tile_as<1, 1, 2, 2, 4, 3, EPI>(p, stream);
     }
     return hipGetLastError();
 }
@@ -592,7 +657,8 @@ hipError_t matmul_as(const Mx4Args& p, int src, hipStream_t stream)
 
 bool mx4_fuses_quantize(int64_t M, int64_t K)
 {
-    return M <= 16 && M * (K / 2 + K / 32) <= 48 * 1024;
+    // beyond this the second launch is cheaper than every workgroup's own pass
+    return M <= 16 && M * K <= 32768;
 }
 
 hipError_t launch_mx4_matmul(const Packed& a, const Packed& b, void* out, bool f32, int64_t M,
