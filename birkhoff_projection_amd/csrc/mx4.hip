@@ -88,8 +88,8 @@ MHC_DEV void finish8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 // bytes per row.
 //
 // LDS: NBUF stage buffers.  A row is 2 KS pieces of 16 bytes, piece c of row r
-// at place c ^ (r % 8) (KS = 2: c ^ (r / 2 % 4)), so that the 8 rows a read
-// phase covers fall on different banks.  Each 4 scale bytes of a row are one
+// at place c ^ (r / 2 % 8) (KS = 2: c ^ (r / 4 % 4)): the 16 rows that one phase
+// of a read covers then fall on all 64 banks.  Each 4 scale bytes of a row are one
 // word; a lane of block half h = lane / 32 shifts it by 8 h and finds the
 // scales of two steps in bytes 0 and 2, which the instruction selects.
 //
@@ -133,7 +133,7 @@ struct Frags {
 template <int KS>
 MHC_DEV int piece_at(int r, int c)
 {
-    return KS == 4 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+    return KS == 4 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
 }
 
 template <int KS, int S, bool TAIL, int TM, int TN>
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
     constexpr int kStep = kBlock / (2 * KS);
     constexpr int NA = BM / kStep, NB = BN / kStep;     // code copies per thread and stage
     constexpr int NX = (ROWS + kBlock - 1) / kBlock;    // scale copies
-    static_assert(BM % kStep == 0 && BN % kStep == 0 && kStep % 8 == 0, "whole copies, one swizzle per thread");
+    static_assert(BM % kStep == 0 && BN % kStep == 0 && kStep % 16 == 0, "whole copies, one swizzle per thread");
     const int row0 = tid / (2 * KS), c16 = 16 * piece_at<KS>(row0, tid % (2 * KS));
     const uint8_t* baseA = p.a + m0 * Kb;
     const uint8_t* baseB = p.b + n0 * Kb;
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
 // launch instead of two, for a call that lasts a few microseconds.
 //
 // LDS per tile: 16 rows of b, then MR rows of a (MR: M rounded up to a power of
-// two), each 128 bytes with piece c of row r at place c ^ (r % 8); then 8 scale
+// two), each 128 bytes with piece c of row r at place c ^ (r / 2 % 8); then 8 scale
 // bytes of each row.  Lanes of rows past M use row M - 1; only their own
 // columns of the result, which are dropped, depend on them.
 // ---------------------------------------------------------------------------
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShap
         for (int q = 64 * wv; q < pieces; q += 256) {
             const int e = q + lane;
             if (e < pieces) {
-                const int r = (e >> 3) & ((1 << lr) - 1), t = e >> (3 + lr), c = (e & 7) ^ (r & 7);
+                const int r = (e >> 3) & ((1 << lr) - 1), t = e >> (3 + lr), c = (e & 7) ^ ((r >> 1) & 7);
                 int64_t kb = (int64_t)(t0 + t) * 128 + 16 * c;
                 kb = kb < Kb ? kb : Kb - 16;  // bytes past the row: not used
                 const int64_t rr = r < have ? r : have - 1;
@@ -545,7 +545,7 @@ __global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShap
                         code = mx_encode8_e2m1(f, amax, s);
                     }
                     const int k = ii[u] >> 2, at = (k >> 3) * MR + mi[u];
-                    *reinterpret_cast<uint32_t*>(sA + at * 128 + 16 * ((k & 7) ^ (mi[u] & 7)) + 4 * (ii[u] & 3)) = code;
+                    *reinterpret_cast<uint32_t*>(sA + at * 128 + 16 * ((k & 7) ^ ((mi[u] >> 1) & 7)) + 4 * (ii[u] & 3)) = code;
                     if ((ii[u] & 3) == 0) xA[at * 8 + (k & 7)] = (uint8_t)s;
                 }
             }
@@ -556,8 +556,8 @@ __global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShap
             for (int s = 0; s < 2; ++s) {
                 const int64_t k = (int64_t)(t0 + t) * 8 + 4 * s + kq;  // this lane's block
                 const bool live = k < Ks;
-                uint4 fb = *reinterpret_cast<const uint4*>(sB + (t * 16 + row) * 128 + 16 * ((4 * s + kq) ^ (row & 7)));
-                uint4 fa = *reinterpret_cast<const uint4*>(sA + (t * MR + ma) * 128 + 16 * ((4 * s + kq) ^ (ma & 7)));
+                uint4 fb = *reinterpret_cast<const uint4*>(sB + (t * 16 + row) * 128 + 16 * ((4 * s + kq) ^ (row >> 1)));
+                uint4 fa = *reinterpret_cast<const uint4*>(sA + (t * MR + ma) * 128 + 16 * ((4 * s + kq) ^ (ma >> 1)));
                 uint32_t xb = *reinterpret_cast<const uint32_t*>(xB + (t * 16 + row) * 8 + 4 * s) >> (8 * kq);
                 uint32_t xa = *reinterpret_cast<const uint32_t*>(xA + (t * MR + ma) * 8 + 4 * s) >> (8 * kq);
                 if (!live) {  // a block past K
