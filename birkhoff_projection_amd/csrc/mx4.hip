@@ -42,43 +42,55 @@ struct Mx4Args {
     int64_t M, N, K;
 };
 
-// 8 consecutive columns (n a multiple of 8) of row m of the product.
-template <int EPI>
-MHC_DEV void finish8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
+// x_out of 8 columns (chunk c) of row m from y and the four streams xq;
+// h: H_post[0..3], then H_res row by row.
+MHC_DEV void write_back8(const Mx4Args& p, int64_t m, int64_t c, const float* y, const uint4 (&xq)[4],
+                         const float4 (&h)[5])
 {
-    if (EPI == kStoreF32) {
-        float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + m * p.N + n);
-        o[0] = make_float4(y[0], y[1], y[2], y[3]);
-        o[1] = make_float4(y[4], y[5], y[6], y[7]);
-        return;
-    }
-    const int64_t N8 = p.N / 8, c = n / 8;
-    if (EPI == kStoreBf16) {
-        reinterpret_cast<uint4*>(p.out)[m * N8 + c] = mx_pack8(y);
-        return;
-    }
+    const int64_t N8 = p.N / 8;
     if (p.out != nullptr) reinterpret_cast<uint4*>(p.out)[m * N8 + c] = mx_pack8(y);
-    uint4 xq[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) xq[j] = mhc_load_stream(&p.x[(m * 4 + j) * N8 + c]);
-    const float4 hp = reinterpret_cast<const float4*>(p.Hpost)[m];
-    const float post[4] = {hp.x, hp.y, hp.z, hp.w};
+    const float post[4] = {h[0].x, h[0].y, h[0].z, h[0].w};
     float xs[4][8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) mx_unpack8(xq[j], xs[j]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 h = reinterpret_cast<const float4*>(p.Hres)[4 * m + i];
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             float s = post[i] * y[e];
-            s = __builtin_fmaf(h.x, xs[0][e], s);
-            s = __builtin_fmaf(h.y, xs[1][e], s);
-            s = __builtin_fmaf(h.z, xs[2][e], s);
-            o[e] = __builtin_fmaf(h.w, xs[3][e], s);
+            s = __builtin_fmaf(h[1 + i].x, xs[0][e], s);
+            s = __builtin_fmaf(h[1 + i].y, xs[1][e], s);
+            s = __builtin_fmaf(h[1 + i].z, xs[2][e], s);
+            o[e] = __builtin_fmaf(h[1 + i].w, xs[3][e], s);
         }
         mhc_store_stream(&p.x_out[(m * 4 + i) * N8 + c], mx_pack8(o));
+    }
+}
+
+// Part q of a row's maps: 0 H_post, 1..4 the rows of H_res.
+MHC_DEV float4 map_part(const Mx4Args& p, int64_t m, int q)
+{
+    return q == 0 ? reinterpret_cast<const float4*>(p.Hpost)[m]
+                  : reinterpret_cast<const float4*>(p.Hres)[4 * m + q - 1];
+}
+
+MHC_DEV void load_x8(const Mx4Args& p, int64_t m, int64_t c, uint4 (&xq)[4])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xq[j] = mhc_load_stream(&p.x[(m * 4 + j) * (p.N / 8) + c]);
+}
+
+// 8 consecutive columns (n a multiple of 8) of row m of the product.
+template <int EPI>
+MHC_DEV void store8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
+{
+    if (EPI == kStoreF32) {
+        float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + m * p.N + n);
+        o[0] = make_float4(y[0], y[1], y[2], y[3]);
+        o[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+        reinterpret_cast<uint4*>(p.out)[m * (p.N / 8) + n / 8] = mx_pack8(y);
     }
 }
 
@@ -187,7 +199,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
     constexpr int kBytes = ROWS * kRowBytes;       // codes of one stage
     constexpr int TS = TN < 2 ? TN : 2;            // tiles side by side in an output strip
     constexpr int kPitch = 32 * TS + 4;            // floats per row of a strip
-    static_assert(WM * WN * 32 * kPitch * 4 <= NBUF * kBytes, "output strips fit the stage buffers");
+    static_assert(WM * WN * 32 * kPitch * 4 + BM * 80 <= NBUF * kBytes,
+                  "output strips and maps fit the stage buffers");
     __shared__ __attribute__((aligned(16))) uint8_t sC[NBUF][kBytes];
     __shared__ uint32_t sX[NBUF][kCopied][ROWS];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -369,14 +382,35 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
     // every wave is done with the stage buffers before they hold the outputs
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     // D: column lane % 32, rows (v % 4) + 8 (v / 4) + 4 (lane / 32).  Strips of
-    // 32 rows go through the wave's own LDS to 8 columns per lane.
+    // 32 rows go through the wave's own LDS to 8 columns per lane.  The
+    // write-back is bound by the memory behind it: the tile's maps are put in
+    // LDS first, and a strip's x is all under way before the strip is written.
     float* strip = reinterpret_cast<float*>(&sC[0][0]) + w * 32 * kPitch;
+    float4* maps = reinterpret_cast<float4*>(&sC[0][0] + WM * WN * 32 * kPitch * 4);  // [BM][5]
+    if constexpr (EPI == kWriteBack) {
+        for (int e = tid; e < BM * 5; e += kBlock) {
+            const int64_t m = m0 + e / 5;
+            maps[e] = map_part(p, m < p.M ? m : p.M - 1, e % 5);
+        }
+        __syncthreads();
+    }
     constexpr int kLanes = 4 * TS;                 // lanes per row
+    constexpr int kQ = 32 * kLanes / 64;           // rows of a strip per lane
     const int64_t mw = m0 + 32 * TM * wm, nw = n0 + 32 * TN * wn;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
 #pragma unroll
         for (int jj = 0; jj < TN; jj += TS) {
+            const int r0 = lane / kLanes, c = 8 * (lane % kLanes);
+            const int64_t n = nw + 32 * jj + c;
+            uint4 xq[kQ][4];
+            if constexpr (EPI == kWriteBack) {
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    const int64_t m = mw + 32 * i + (64 / kLanes) * q + r0;
+                    load_x8(p, m < p.M ? m : p.M - 1, (n < p.N ? n : p.N - 8) / 8, xq[q]);
+                }
+            }
             mhc_wave_lds_fence();  // the previous strip's reads come first
 #pragma unroll
             for (int j = 0; j < TS; ++j)
@@ -385,14 +419,19 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
                     strip[((v & 3) + 8 * (v >> 2) + 4 * kh) * kPitch + 32 * j + (lane & 31)] = acc[i][jj + j][v];
             mhc_wave_lds_fence();
 #pragma unroll
-            for (int q = 0; q < 32 * kLanes / 64; ++q) {
-                const int r = (64 / kLanes) * q + lane / kLanes, c = 8 * (lane % kLanes);
-                const int64_t m = mw + 32 * i + r, n = nw + 32 * jj + c;
+            for (int q = 0; q < kQ; ++q) {
+                const int r = (64 / kLanes) * q + r0;
+                const int64_t m = mw + 32 * i + r;
                 if (m < p.M && n < p.N) {
                     const float4 y0 = *reinterpret_cast<const float4*>(&strip[r * kPitch + c]);
                     const float4 y1 = *reinterpret_cast<const float4*>(&strip[r * kPitch + c + 4]);
                     const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-                    finish8<EPI>(p, m, n, y);
+                    if constexpr (EPI == kWriteBack) {
+                        const float4* h = maps + 5 * (m - m0);
+                        write_back8(p, m, n / 8, y, xq[q], {h[0], h[1], h[2], h[3], h[4]});
+                    } else {
+                        store8<EPI>(p, m, n, y);
+                    }
                 }
             }
         }
@@ -586,7 +625,15 @@ __global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShap
                 for (int ww = 0; ww < kFewWaves; ++ww) s += sR[ww][tid >> 1][8 * (tid & 1) + e];
                 y[e] = s;
             }
-            finish8<EPI>(p, m, nn, y);
+            if constexpr (EPI == kWriteBack) {
+                uint4 xq[4];
+                load_x8(p, m, nn / 8, xq);
+                write_back8(p, m, nn / 8, y, xq,
+                            {map_part(p, m, 0), map_part(p, m, 1), map_part(p, m, 2), map_part(p, m, 3),
+                             map_part(p, m, 4)});
+            } else {
+                store8<EPI>(p, m, nn, y);
+            }
         }
     }
 }
