@@ -126,6 +126,25 @@ def lib():
     return _lib
 
 
+_binding = None
+
+
+def binding():
+    """The extension module that marshals tensors for the packed calls (raises
+    if it is not built)."""
+    global _binding
+    if _binding is None:
+        lib()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError(
+                f"{os.path.join(_HERE, '_binding.so')} is missing or does not load: build it with "
+                "`python -m birkhoff_projection_amd.build`") from e
+        _binding = module
+    return _binding
+
+
 def check(status: int) -> None:
     if status != 0:
         msg = lib().mhc_last_error().decode(errors="replace")

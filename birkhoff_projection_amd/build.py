@@ -1,4 +1,5 @@
-"""Build the gfx950 shared library ``libmhc.so`` in-tree with hipcc.
+"""Build the gfx950 shared library ``libmhc.so`` in-tree with hipcc, and the
+extension module ``_binding.so`` that marshals PyTorch tensors to it.
 
 Every HIP source is compiled for gfx950 only, with packed-fp32 code
 generation switched off (``-target-feature -packed-fp32-ops``), then linked
@@ -19,6 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmhc.so")
 SOURCES = ["abi.hip", "birkhoff.hip", "birkhoffn.hip", "mix.hip", "layer.hip", "ckpt.hip",
            "layer_ckpt.hip", "read.hip", "mx4.hip"]
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = "gfx950"
 
 
@@ -36,12 +38,38 @@ def compile_flags():
             "-Wall", "-Wno-unused-function"]
 
 
+def binding_command(obj: str):
+    """Compile command of csrc/binding.cpp (host code only, against torch)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    cxx = shutil.which("g++") or shutil.which("clang++")
+    if cxx is None:
+        raise RuntimeError("no C++ compiler: the tensor binding cannot be built")
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + \
+        [f"-isystem{p}" for p in inc] + ["-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+
+
+def binding_link(obj: str, out: str):
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++" if shutil.which("g++") else "clang++", "-shared", "-o", out, obj, LIB, f"-L{lib}",
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link ``libmhc.so``; returns its path."""
+    """Compile every source and link ``libmhc.so`` and ``_binding.so``; returns
+    the library's path."""
     cc = hipcc()
     os.makedirs(BUILD, exist_ok=True)
     procs = []
     objs = []
+    bobj = os.path.join(BUILD, "binding.o")
+    procs.append(("binding.cpp", subprocess.Popen(binding_command(bobj), stdout=subprocess.PIPE,
+                                                  stderr=subprocess.STDOUT, text=True)))
     for src in SOURCES:
         obj = os.path.join(BUILD, src.replace(".hip", ".o"))
         objs.append(obj)
@@ -58,13 +86,16 @@ def build(verbose: bool = False) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"hipcc failed for {failed}")
+        raise RuntimeError(f"compilation failed for {failed}")
     tmp = LIB + ".tmp"
-    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-o", tmp] + objs
+    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-Wl,-soname,libmhc.so", "-o", tmp] + objs
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    tmp = BINDING + ".tmp"
+    subprocess.run(binding_link(bobj, tmp), check=True)
+    os.replace(tmp, BINDING)
     return LIB
 
 
