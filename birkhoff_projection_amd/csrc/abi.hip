@@ -650,6 +650,10 @@ mhc_status mhc_layer_fwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* k, 
     if (s != MHC_OK) return s;
     if (a->T == 0) return ok();
     const size_t T = (size_t)a->T, C = (size_t)a->C;
+    const int64_t need = mhc::read_plan(a->T, a->C).bytes;
+    if (need > 0 && a->workspace_bytes < need)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "workspace_bytes=%lld < %lld required",
+                    (long long)a->workspace_bytes, (long long)need);
     const Buf b[] = {{a->x, T * 4 * C * 2, "x"},
                      {a->W, 24 * 4 * C * 2, "W"},
                      {a->f, T * C * 2, "f"},
@@ -663,12 +667,13 @@ mhc_status mhc_layer_fwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* k, 
                      {k->x_codes, T * 4 * C, "x_codes"},
                      {k->x_scales, T * 4 * (C / 32), "x_scales"},
                      {k->f_codes, T * C, "f_codes"},
-                     {k->f_scales, T * (C / 32), "f_scales"}};
-    s = check_buffers(b, sizeof(b) / sizeof(b[0]));
+                     {k->f_scales, T * (C / 32), "f_scales"},
+                     {a->workspace, (size_t)need, "workspace"}};
+    s = check_buffers(b, (int)(sizeof(b) / sizeof(b[0])) - (need > 0 ? 0 : 1));
     if (s != MHC_OK) return s;
     const mhc::LayerPtrs p{a->x,   a->W,      a->f,     a->u,     a->x_out, a->rms,
                            a->logits, a->H_pre, a->H_post, a->H_res, nullptr, nullptr,
-                           nullptr, nullptr,  nullptr,  nullptr,  nullptr};
+                           nullptr, nullptr,  nullptr,  nullptr,  a->workspace};
     return launched(mhc::launch_layer_fwd_ckpt(p, mhc::Packed{k->x_codes, k->x_scales},
                                                mhc::Packed{k->f_codes, k->f_scales}, a->T, a->C,
                                                a->eps, k->format, o, (hipStream_t)stream),

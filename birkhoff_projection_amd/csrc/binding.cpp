@@ -225,6 +225,19 @@ mhc_layer_args layer_args(const Shape3& s, double eps, const mhc_proj_opts* opts
     return a;
 }
 
+// The workspace of the maps, if the shape needs one, set in a.
+Tensor read_workspace(mhc_layer_args& a, const Tensor& like)
+{
+    Tensor ws;
+    const int64_t n = mhc_layer_read_workspace_bytes(a.T, a.n, a.C);
+    if (n > 0) {
+        ws = at::empty({n}, like.options().dtype(at::kByte));
+        a.workspace = ws.data_ptr();
+        a.workspace_bytes = n;
+    }
+    return ws;
+}
+
 // maps_out: empty or 5 optional buffers; outs: u, x_out; ckpt: x codes, x
 // scales, f codes, f scales.
 std::tuple<int, std::vector<Tensor>, std::vector<Tensor>, std::vector<Tensor>> layer_fwd_ckpt(
@@ -250,6 +263,7 @@ std::tuple<int, std::vector<Tensor>, std::vector<Tensor>, std::vector<Tensor>> l
     a.u = o[0].data_ptr();
     a.x_out = o[1].data_ptr();
     set_maps(a, maps);
+    const Tensor ws = read_workspace(a, x);
     const mhc_layer_ckpt k{format, c[0].data_ptr(), u8_out(c[1]), c[2].data_ptr(), u8_out(c[3])};
     const int st = mhc_layer_fwd_ckpt(&a, &k, stream_of(x));
     return {st, std::move(maps), std::move(o), std::move(c)};
@@ -326,13 +340,7 @@ std::tuple<int, std::vector<Tensor>, Opt, Opt, Opt> layer_read(
     a.W = W.const_data_ptr();
     a.u = u ? u->data_ptr() : nullptr;
     set_maps(a, maps);
-    const int64_t n = mhc_layer_read_workspace_bytes(s.T, (int32_t)s.n, s.C);
-    Tensor ws;
-    if (n > 0) {
-        ws = at::empty({n}, x.options().dtype(at::kByte));
-        a.workspace = ws.data_ptr();
-        a.workspace_bytes = n;
-    }
+    const Tensor ws = read_workspace(a, x);
     const int st = mhc_layer_read(&a, codes ? codes->data_ptr() : nullptr, scales ? u8_out(*scales) : nullptr,
                                   stream_of(x));
     return {st, std::move(maps), std::move(u), std::move(codes), std::move(scales)};

@@ -6,8 +6,9 @@
 //          sigmoid derivative and projection backward -> grad_logits
 //   dx     grad_x, grad_f
 //   dw     grad_W partials on MFMA
-// The maps pass of the forward, the transposition of W and the reduction of
-// the grad_W partials are the plain layer's.
+// The maps of the forward are the layer's read half's (read.hip); the
+// transposition of W and the reduction of the grad_W partials are the plain
+// layer's.
 //
 // The formulas are the plain layer's with xhat, fhat (what the checkpoints
 // stand for) in the place of x, f; the forward's r, logits and maps are those
@@ -265,14 +266,82 @@ MHC_DEV void dots_consume(const DotsLane& L, const DotsLoads& d, const DotsStep&
     }
 }
 
+// What a token's dots become: sigmoid derivative, projection backward, the
+// RMSNorm coefficient, and dl / r as the operand of the grad_W pass.
+struct DotsOut {
+    const float* Hpre;
+    const float* Hpost;
+    const float* Hres;
+    const float* logits;
+    const float* rms;
+    float* glogits;
+    float* svec;
+    __bf16* dlT;
+    int64_t T, D;  // tokens; D = 4C
+};
+
+// One lane finishes token t (tokens from T on: zeros for the grad_W pass).
+MHC_DEV void finish_token(const DotsOut& o, int64_t t, const float* dots)
+{
+    float dl[kMaps];
+    if (t < o.T) {
+        float d[kMaps];
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) d[m] = dots[m];
+        const float4 pq = reinterpret_cast<const float4*>(o.Hpre)[t];
+        const float4 oq = reinterpret_cast<const float4*>(o.Hpost)[t];
+        const float hp[4] = {pq.x, pq.y, pq.z, pq.w};
+        const float ho[4] = {oq.x, oq.y, oq.z, oq.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            dl[j] = d[j] * hp[j] * (1.f - hp[j]);
+            dl[4 + j] = d[4 + j] * ho[j] * (1.f - ho[j]);
+        }
+        float H[16];
+        const float4* hr = reinterpret_cast<const float4*>(o.Hres + 16 * t);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 v = hr[q];
+            H[4 * q] = v.x;
+            H[4 * q + 1] = v.y;
+            H[4 * q + 2] = v.z;
+            H[4 * q + 3] = v.w;
+        }
+        project_bwd_refined(H, d + 8, dl + 8);
+        // RMSNorm coefficient: <dl W, x / r> / (4C) = <dl, logits> / (4C)
+        float s = 0.f;
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) s = __builtin_fmaf(dl[m], o.logits[kMaps * t + m], s);
+        o.svec[t] = s / (float)o.D;
+        float4* go = reinterpret_cast<float4*>(o.glogits + kMaps * t);
+#pragma unroll
+        for (int q = 0; q < kMaps / 4; ++q) go[q] = make_float4(dl[4 * q], dl[4 * q + 1], dl[4 * q + 2], dl[4 * q + 3]);
+        const float inv = 1.f / o.rms[t];
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) dl[m] *= inv;
+    } else {
+#pragma unroll
+        for (int m = 0; m < kMaps; ++m) dl[m] = 0.f;
+    }
+#pragma unroll
+    for (int m = 0; m < kMaps; ++m) {
+        float v = dl[m];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+            const __bf16 h = (__bf16)v;
+            o.dlT[dl_at(t, p, m)] = h;
+            v -= (float)h;
+        }
+    }
+}
+
 template <int FMT>
 __global__ __launch_bounds__(kBlock) void layer_dots_ckpt_kernel(
     const uint2* __restrict__ xc, const uint8_t* __restrict__ xs, const uint2* __restrict__ fc,
     const uint8_t* __restrict__ fs, const uint4* __restrict__ gxo, const uint4* __restrict__ gu,
-    const float* __restrict__ Hpre, const float* __restrict__ Hpost, const float* __restrict__ Hres,
-    const float* __restrict__ logits, const float* __restrict__ rms, float* __restrict__ glogits,
-    float* __restrict__ svec, __bf16* __restrict__ dlT, int64_t T, int64_t Tp, int64_t C8, int tw)
+    DotsOut o, int64_t Tp, int64_t C8, int tw)
 {
+    const int64_t T = o.T;
     __shared__ float sDots[4][16][kMaps];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t tb = ((int64_t)blockIdx.x * 4 + w) * tw;
@@ -302,61 +371,60 @@ __global__ __launch_bounds__(kBlock) void layer_dots_ckpt_kernel(
     if (lane >= tw) return;
     const int64_t t = tb + lane;
     if (t >= Tp) return;
-    float dl[kMaps];
-    if (t < T) {
-        float d[kMaps];
+    finish_token(o, t, sDots[w][lane]);
+}
+
+// Few tokens of a wide layer: a workgroup per token, its 4 waves share the
+// chunks (one wave per token walks 7168 columns in 14 dependent steps).
+template <int FMT>
+__global__ __launch_bounds__(kBlock) void layer_dots_few_ckpt_kernel(
+    const uint2* __restrict__ xc, const uint8_t* __restrict__ xs, const uint2* __restrict__ fc,
+    const uint8_t* __restrict__ fs, const uint4* __restrict__ gxo, const uint4* __restrict__ gu,
+    DotsOut o, int64_t C8)
+{
+    __shared__ float sDots[4][kMaps];
+    __shared__ float sSum[kMaps];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t t = blockIdx.x;
+    if (t < o.T) {
+        DotsLane L;
+        L.xc = xc; L.xs = xs; L.fc = fc; L.fs = fs; L.gxo = gxo; L.gu = gu;
+        L.T = o.T; L.C8 = C8; L.tb = t; L.lane = lane;
+        float acc[32];
 #pragma unroll
-        for (int m = 0; m < kMaps; ++m) d[m] = sDots[w][lane][m];
-        const float4 pq = reinterpret_cast<const float4*>(Hpre)[t];
-        const float4 oq = reinterpret_cast<const float4*>(Hpost)[t];
-        const float hp[4] = {pq.x, pq.y, pq.z, pq.w};
-        const float ho[4] = {oq.x, oq.y, oq.z, oq.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            dl[j] = d[j] * hp[j] * (1.f - hp[j]);
-            dl[4 + j] = d[4 + j] * ho[j] * (1.f - ho[j]);
+        for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+        const int nch = (int)((C8 + 63) / 64);
+        L.nch = nch + 1;  // no chunk is "the last": the reduction is here
+        DotsLoads d0, d1;
+        DotsStep s0{0, w};
+        dots_issue(L, d0, s0);
+        while (s0.ci < nch) {
+            const DotsStep s1{0, s0.ci + 4}, s2{0, s0.ci + 8};
+            dots_issue(L, d1, s1);
+            __builtin_amdgcn_sched_barrier(0);
+            dots_consume<FMT>(L, d0, s0, acc, nullptr);
+            __builtin_amdgcn_sched_barrier(0);
+            dots_issue(L, d0, s2);
+            __builtin_amdgcn_sched_barrier(0);
+            if (s1.ci < nch) dots_consume<FMT>(L, d1, s1, acc, nullptr);
+            __builtin_amdgcn_sched_barrier(0);
+            s0 = s2;
         }
-        float H[16];
-        const float4* hr = reinterpret_cast<const float4*>(Hres + 16 * t);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float4 v = hr[q];
-            H[4 * q] = v.x;
-            H[4 * q + 1] = v.y;
-            H[4 * q + 2] = v.z;
-            H[4 * q + 3] = v.w;
-        }
-        project_bwd_refined(H, d + 8, dl + 8);
-        // RMSNorm coefficient: <dl W, x / r> / (4C) = <dl, logits> / (4C)
-        float s = 0.f;
-#pragma unroll
-        for (int m = 0; m < kMaps; ++m) s = __builtin_fmaf(dl[m], logits[kMaps * t + m], s);
-        svec[t] = s / (float)(32 * C8);
-        float4* go = reinterpret_cast<float4*>(glogits + kMaps * t);
-#pragma unroll
-        for (int q = 0; q < kMaps / 4; ++q) go[q] = make_float4(dl[4 * q], dl[4 * q + 1], dl[4 * q + 2], dl[4 * q + 3]);
-        const float inv = 1.f / rms[t];
-#pragma unroll
-        for (int m = 0; m < kMaps; ++m) dl[m] *= inv;
-    } else {
-#pragma unroll
-        for (int m = 0; m < kMaps; ++m) dl[m] = 0.f;
+        const float sm = wave_sum_halving<32>(acc);
+        const int idx = (lane >> 1) & 31;
+        if ((lane & 1) == 0 && idx < kMaps) sDots[w][idx] = sm;
     }
-#pragma unroll
-    for (int m = 0; m < kMaps; ++m) {
-        float v = dl[m];
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            const __bf16 h = (__bf16)v;
-            dlT[dl_at(t, p, m)] = h;
-            v -= (float)h;
-        }
-    }
+    __syncthreads();
+    if (threadIdx.x < kMaps)
+        sSum[threadIdx.x] = (sDots[0][threadIdx.x] + sDots[1][threadIdx.x]) +
+                            (sDots[2][threadIdx.x] + sDots[3][threadIdx.x]);
+    __syncthreads();
+    if (threadIdx.x == 0) finish_token(o, t, sSum);
 }
 
 // ---------------------------------------------------------------------------
-// dx: workgroup = 16 tokens x all columns, in chunks of 128 columns of every
-// stream.  Per chunk wave w forms (dl W)^T of stream w on MFMA (16 k x 16
+// dx: workgroup = 16 tokens x a range of the columns (all of them unless the
+// tokens are few), in chunks of 128 columns of every stream.  Per chunk wave w forms (dl W)^T of stream w on MFMA (16 k x 16
 // tokens, A from the transposed W, B = dl in two bf16 parts, fixed for the
 // workgroup) into LDS; then an element-wise pass with lane = (token, 8
 // columns) whose accesses cover 4 rows x 256 contiguous bytes.  All loads of
@@ -474,7 +542,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
     const uint4* __restrict__ gu, const uint4* __restrict__ Wt, const float* __restrict__ Hpre,
     const float* __restrict__ Hpost, const float* __restrict__ Hres, const float* __restrict__ rms,
     const float* __restrict__ glogits, const float* __restrict__ svec, uint4* __restrict__ gx,
-    uint4* __restrict__ gf, int64_t T, int64_t C)
+    uint4* __restrict__ gf, int64_t T, int64_t C, int64_t per)
 {
     __shared__ __attribute__((aligned(16))) float sD[2][kDxTok][kDxPitch];
     DxLane L;
@@ -524,12 +592,14 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
         L.inv = 1.f / rms[L.tr];
         L.sr = svec[L.tr] * L.inv;
     }
-    // branch-free pipeline: the chunk count is padded to even, chunks past C
-    // load clamped addresses and do no element-wise work
-    const int64_t n = (C + kDxChunk - 1) / kDxChunk;
+    // branch-free pipeline: chunk counts are even, chunks past C load clamped
+    // addresses and do no element-wise work
+    const int64_t first = (int64_t)blockIdx.y * per;
+    int64_t n = first + per;
+    if (n * kDxChunk > C) n = (C + kDxChunk - 1) / kDxChunk;
     DxLoads d0, d1;
-    dx_issue(L, d0, 0);
-    for (int64_t ci = 0; ci < n; ci += 2) {
+    dx_issue(L, d0, first * kDxChunk);
+    for (int64_t ci = first; ci < n; ci += 2) {
         dx_issue(L, d1, (ci + 1) * kDxChunk);
         __builtin_amdgcn_sched_barrier(0);
         dx_consume<FMT>(L, d0, sD[0], ci * kDxChunk);
@@ -675,6 +745,8 @@ __global__ __launch_bounds__(kBlock) void layer_dw_ckpt_kernel(
     }
 }
 
+constexpr int64_t kFewTokens = 2048;
+
 template <int FMT>
 hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, int64_t T, int64_t C,
                         hipStream_t stream)
@@ -686,20 +758,32 @@ hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, in
     uint4* wt = reinterpret_cast<uint4*>(ws + p.off_wt);
     float* partial = reinterpret_cast<float*>(ws + p.off_partial);
     const uint2* xc = static_cast<const uint2*>(x.codes);
-    int tw = 16;  // tokens per wave: a workgroup for every compute unit where there are as many tokens
-    while (tw > 1 && p.Tp / (4 * tw) < 256) tw /= 2;
-    hipLaunchKernelGGL(layer_dots_ckpt_kernel<FMT>, dim3((unsigned)(p.Tp / (4 * tw))), dim3(kBlock), 0,
-                       stream, xc, x.scales, static_cast<const uint2*>(f.codes), f.scales,
-                       (const uint4*)a.grad_x_out, (const uint4*)a.grad_u, a.H_pre, a.H_post,
-                       a.H_res, a.logits, a.rms, a.grad_logits, svec, dlT, T, p.Tp, C / 8, tw);
+    const DotsOut o{a.H_pre, a.H_post, a.H_res, a.logits, a.rms, a.grad_logits, svec, dlT, T, 4 * C};
+    const uint2* fc = static_cast<const uint2*>(f.codes);
+    const uint4* gxo = static_cast<const uint4*>(a.grad_x_out);
+    const uint4* gu = static_cast<const uint4*>(a.grad_u);
+    if (T <= kFewTokens && C > 512) {
+        hipLaunchKernelGGL(layer_dots_few_ckpt_kernel<FMT>, dim3((unsigned)p.Tp), dim3(kBlock), 0, stream,
+                           xc, x.scales, fc, f.scales, gxo, gu, o, C / 8);
+    } else {
+        int tw = 16;  // tokens per wave: a workgroup for every compute unit where there are as many tokens
+        while (tw > 1 && p.Tp / (4 * tw) < 256) tw /= 2;
+        hipLaunchKernelGGL(layer_dots_ckpt_kernel<FMT>, dim3((unsigned)(p.Tp / (4 * tw))), dim3(kBlock), 0,
+                           stream, xc, x.scales, fc, f.scales, gxo, gu, o, p.Tp, C / 8, tw);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     e = launch_layer_wt(a.W, wt, C, stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(layer_dx_ckpt_kernel<FMT>, dim3((unsigned)((T + kDxTok - 1) / kDxTok)),
-                       dim3(kBlock), 0, stream, xc, x.scales, (const uint4*)a.grad_x_out,
-                       (const uint4*)a.grad_u, wt, a.H_pre, a.H_post, a.H_res, a.rms, a.grad_logits,
-                       svec, (uint4*)a.grad_x, (uint4*)a.grad_f, T, C);
+    // column ranges of whole pairs of chunks, for about 512 workgroups
+    const int64_t tiles = (T + kDxTok - 1) / kDxTok, pairs = (C + 2 * kDxChunk - 1) / (2 * kDxChunk);
+    int64_t ranges = (512 + tiles - 1) / tiles;
+    ranges = ranges < pairs ? ranges : pairs;
+    const int64_t per = 2 * ((pairs + ranges - 1) / ranges);
+    ranges = (2 * pairs + per - 1) / per;
+    hipLaunchKernelGGL(layer_dx_ckpt_kernel<FMT>, dim3((unsigned)tiles, (unsigned)ranges), dim3(kBlock), 0,
+                       stream, xc, x.scales, gxo, gu, wt, a.H_pre, a.H_post, a.H_res, a.rms,
+                       a.grad_logits, svec, (uint4*)a.grad_x, (uint4*)a.grad_f, T, C, per);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(layer_dw_ckpt_kernel<FMT>, dim3((unsigned)(4 * C / (2 * kDwK)), (unsigned)p.groups),
@@ -743,7 +827,7 @@ hipError_t launch_layer_fwd_ckpt(const LayerPtrs& a, const Packed& x, const Pack
                                  int64_t C, float eps, int fmt, const SolverOpts& o,
                                  hipStream_t stream)
 {
-    const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
+    const hipError_t e = launch_maps(a, T, C, eps, o, stream);
     if (e != hipSuccess) return e;
     return fmt == kE4M3 ? layer_mix_as<kE4M3>(a, x, f, T, C, stream)
                         : layer_mix_as<kInt8>(a, x, f, T, C, stream);

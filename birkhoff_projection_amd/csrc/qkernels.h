@@ -69,6 +69,9 @@ struct ReadPlan {
     int64_t splits, steps_per, bytes;
 };
 ReadPlan read_plan(int64_t T, int64_t C);
+// The maps alone (the same as launch_layer_read's), with the same workspace.
+hipError_t launch_maps(const LayerPtrs& a, int64_t T, int64_t C, float eps, const SolverOpts& o,
+                       hipStream_t stream);
 hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, int64_t C, float eps,
                              const SolverOpts& o, hipStream_t stream);
 

@@ -198,6 +198,7 @@ __global__ __launch_bounds__(kBlock) void read_finish_kernel(
         }
         return;
     }
+    if (o.u == nullptr && o.codes == nullptr) return;  // the maps alone
     float M[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) M[j] = sigmoid(sL[j] * inv);
@@ -218,7 +219,7 @@ constexpr int64_t kReadFewTokens = 2048;
 ReadPlan read_plan(int64_t T, int64_t C)
 {
     ReadPlan p{0, 0, 0};
-    if (T > kReadFewTokens) return p;
+    if (T <= 0 || T > kReadFewTokens) return p;
     const int64_t steps = 4 * C / 32, tiles = (T + kPartTok - 1) / kPartTok;
     int64_t want = (512 + tiles - 1) / tiles;
     if (want > steps / 16) want = steps / 16;
@@ -229,18 +230,10 @@ ReadPlan read_plan(int64_t T, int64_t C)
     return p;
 }
 
-hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, int64_t C, float eps,
-                             const SolverOpts& o, hipStream_t stream)
+// Few tokens: maps, and u where `uo` has a place for it.
+static hipError_t launch_split(const LayerPtrs& a, const ReadPlan& p, const UOut& uo, int64_t T,
+                               int64_t C, float eps, const SolverOpts& o, hipStream_t stream)
 {
-    const UOut uo{(uint4*)a.u, (uint32_t*)u4.codes, u4.scales};
-    const ReadPlan p = read_plan(T, C);
-    if (p.splits == 0) {
-        const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(read_mix_kernel, dim3(token_grid(T)),
-                           dim3(kBlock), 0, stream, (const uint4*)a.x, a.H_pre, uo, T, C / 8);
-        return hipGetLastError();
-    }
     float* partial = static_cast<float*>(a.workspace);
     hipLaunchKernelGGL(read_part_kernel,
                        dim3((unsigned)((T + kPartTok - 1) / kPartTok), (unsigned)p.splits),
@@ -256,6 +249,27 @@ hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, in
         hipLaunchKernelGGL(read_finish_kernel<1>, dim3((unsigned)T), dim3(kBlock), 0, stream,
                            (const uint4*)a.x, partial, (int)p.splits, a.logits, a.rms, a.H_pre,
                            a.H_post, a.H_res, uo, T, C / 8, eps, o);
+    return hipGetLastError();
+}
+
+hipError_t launch_maps(const LayerPtrs& a, int64_t T, int64_t C, float eps, const SolverOpts& o,
+                       hipStream_t stream)
+{
+    const ReadPlan p = read_plan(T, C);
+    if (p.splits == 0) return launch_layer_maps(a, T, C, eps, o, stream);
+    return launch_split(a, p, UOut{nullptr, nullptr, nullptr}, T, C, eps, o, stream);
+}
+
+hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, int64_t C, float eps,
+                             const SolverOpts& o, hipStream_t stream)
+{
+    const UOut uo{(uint4*)a.u, (uint32_t*)u4.codes, u4.scales};
+    const ReadPlan p = read_plan(T, C);
+    if (p.splits != 0) return launch_split(a, p, uo, T, C, eps, o, stream);
+    const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(read_mix_kernel, dim3(token_grid(T)), dim3(kBlock), 0, stream,
+                       (const uint4*)a.x, a.H_pre, uo, T, C / 8);
     return hipGetLastError();
 }
 

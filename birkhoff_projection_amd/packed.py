@@ -133,10 +133,11 @@ def projected_mix(x, logits, *, format="e4m3", **opts):
 def layer_fwd_ckpt(x, W, f, *, format="e4m3", eps=1e-6, solver="newton", max_iters=None, tol=None,
                    warm_sweeps=None, out=None, ckpt=None):
     """``layer_fwd`` that also writes the checkpoints of x and f.  Returns
-    (forward dict, dict(x=(codes, scales), f=(codes, scales))); the forward's
-    outputs are layer_fwd's bit for bit.  Only the checkpoints and the
-    forward's rms, logits and maps are needed by layer_bwd_ckpt.  ``out`` and
-    ``ckpt`` may be previous results."""
+    (forward dict, dict(x=(codes, scales), f=(codes, scales))).  The maps are
+    layer_read's bit for bit, and above 2048 tokens all of the forward is
+    layer_fwd's.  Only the checkpoints and the forward's rms, logits and maps
+    are needed by layer_bwd_ckpt.  ``out`` and ``ckpt`` may be previous
+    results."""
     out, ckpt = out or {}, ckpt or {}
     status, maps, (u, x_out), k = binding().layer_fwd_ckpt(
         x, W, f, _format(format), eps, _opts(solver, max_iters, tol, warm_sweeps),

@@ -467,8 +467,13 @@ typedef struct {
 } mhc_layer_ckpt;
 
 /* mhc_layer_fwd_ckpt -- mhc_layer_fwd that also writes the checkpoints of x
- * and f, in the pass that reads both; its other outputs are mhc_layer_fwd's,
- * bit for bit.  No output may overlap another tensor. */
+ * and f, in the pass that reads both.  rms, logits and the maps are
+ * mhc_layer_read's, with its workspace in a->workspace (a->workspace_bytes at
+ * least mhc_layer_read_workspace_bytes(), 0 above 2048 tokens): above 2048
+ * tokens every output is mhc_layer_fwd's bit for bit, below the sums behind
+ * the maps are added in another order.  No output may overlap another tensor;
+ * the workspace must not be in use by another call that overlaps on the
+ * device. */
 mhc_status mhc_layer_fwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* ckpt, void* stream);
 
 /* mhc_layer_bwd_ckpt -- mhc_layer_bwd from the checkpoints: xhat and fhat in

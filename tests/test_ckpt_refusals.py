@@ -103,6 +103,12 @@ def test_layer_errors(L):
         assert f(ctypes.byref(a), ctypes.byref(k), None) == UNSUPPORTED
         a, k = _layer(T=0)
         assert f(ctypes.byref(a), ctypes.byref(k), None) == 0
+    assert L.mhc_layer_read_workspace_bytes(0, 4, 64) == 0  # no tokens
+    assert L.mhc_layer_read_workspace_bytes(2049, 4, 64) == 0
+    a, k = _layer()
+    a.workspace_bytes = L.mhc_layer_read_workspace_bytes(16, 4, 64) - 1
+    assert L.mhc_layer_fwd_ckpt(ctypes.byref(a), ctypes.byref(k), None) == INVALID
+    assert "workspace_bytes" in _err(L)
     a, k = _layer()
     a.eps = 0.0
     assert L.mhc_layer_fwd_ckpt(ctypes.byref(a), ctypes.byref(k), None) == INVALID

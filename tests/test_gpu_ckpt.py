@@ -220,6 +220,23 @@ def _layer_case(T, C, seed, wscale=1.0):
             bf(g.standard_normal((T, 4, C))), bf(g.standard_normal((T, C))))
 
 
+def check_layer_fwd(gpu_lib, fw, x, Wt, f):
+    """The forward beside the checkpoints: the read half's maps and u bit for
+    bit, above 2048 tokens all of layer_fwd's; x_out from those maps."""
+    T = x.shape[0]
+    read = gpu_lib.layer_read(x, Wt)
+    for k in read:
+        assert torch.equal(fw[k], read[k]), k
+    if T > 2048:
+        fw0 = gpu_lib.layer_fwd(x, Wt, f)
+        for k in fw0:
+            assert torch.equal(fw[k], fw0[k]), k
+    post, res = fw["H_post"].double()[:, :, None], fw["H_res"].double()
+    ref = post * f.double()[:, None] + torch.matmul(res, x.double())
+    mag = post * f.double().abs()[:, None] + torch.matmul(res, x.double().abs())
+    assert bool(((fw["x_out"].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 5 * U * mag).all())
+
+
 def check_layer_bwd(bw, fwd, xh, W64, fh, g64, u64):
     """The layer backward's outputs against the oracle for xhat, fhat and the
     kernel's own forward maps."""
@@ -252,14 +269,13 @@ def check_layer_bwd(bw, fwd, xh, W64, fh, g64, u64):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("T,C", [(1, 64), (37, 64), (64, 128), (130, 192), (300, 576), (2048, 256)])
+@pytest.mark.parametrize("T,C", [(1, 64), (37, 64), (64, 128), (130, 192), (300, 576), (2048, 256), (1, 7168), (5, 1088), (66, 2624),
+                                 (2049, 576), (2100, 64)])
 def test_layer_ckpt(gpu_lib, T, C, fmt):
     print(f"layer ckpt T={T} C={C} {fmt}", flush=True)
     x, Wt, f, g, du = _layer_case(T, C, T + C)
     fw, ck = gpu_lib.layer_fwd_ckpt(x, Wt, f, format=fmt)
-    fw0 = gpu_lib.layer_fwd(x, Wt, f)
-    for k in fw0:
-        assert torch.equal(fw[k], fw0[k]), k
+    check_layer_fwd(gpu_lib, fw, x, Wt, f)
     for k, t in (("x", x), ("f", f)):
         c, s = gpu_lib.ckpt_pack(t, format=fmt)
         assert torch.equal(ck[k][0], c) and torch.equal(ck[k][1], s), k
