@@ -252,7 +252,9 @@ __global__ __launch_bounds__(kBlock) void pack_transposed_kernel(
 // Stream mix with checkpoint.  Forward: tokens b, b + G, ... of a grid of G
 // workgroups, as in the plain stream mix (the workgroups then stream a
 // contiguous front of the tensors); per chunk of 8 columns the four streams
-// are mixed and each is packed from the same registers.
+// are mixed and each is packed from the same registers.  Where a row has
+// fewer than 256 chunks, 2^shift threads share a token and the workgroup
+// takes several tokens at once.
 // ---------------------------------------------------------------------------
 constexpr int kTokensPerBlock = 16;
 
@@ -275,10 +277,11 @@ MHC_DEV void mix_rows(const float* M, const float (*x)[8], uint4* o)
 
 // H_out may be the logits buffer itself (a lane reads its token's logits
 // before it writes that token's H), so neither pointer is declared restrict.
-template <int PROJ, int FMT>
+template <int PROJ, int FMT, bool NARROW>
 __global__ __launch_bounds__(kBlock) void stream_mix_ckpt_kernel(
     const uint4* __restrict__ x, const float* Hl, float* H_out, uint4* __restrict__ out,
-    uint2* __restrict__ codes, uint8_t* __restrict__ scales, int64_t T, int64_t C8, SolverOpts o)
+    uint2* __restrict__ codes, uint8_t* __restrict__ scales, int64_t T, int64_t C8, int shift,
+    SolverOpts o)
 {
     __shared__ float sH[kTokensPerBlock][16];
     const int64_t b = blockIdx.x, G = gridDim.x;
@@ -318,14 +321,14 @@ __global__ __launch_bounds__(kBlock) void stream_mix_ckpt_kernel(
     __syncthreads();
 
     const int64_t Cb = (C8 + 3) / 4;  // blocks per stream row
-    for (int tl = 0; tl < nt; ++tl) {
+    for (int tl = first_token<NARROW>(tid, shift); tl < nt; tl += kBlock >> shift) {
         float M[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) M[k] = sH[tl][k];
         const int64_t row = (b + G * tl) * 4;
         // the last block of a row may be part empty: its quad runs whole,
         // with zeros in the empty chunks
-        for (int64_t c = tid; c < 4 * Cb; c += kBlock) {
+        for (int64_t c = tid & ((1 << shift) - 1); c < 4 * Cb; c += 1 << shift) {
             const bool in = c < C8;
             const int64_t cc = in ? c : C8 - 1;
             uint4 xin[4], oo[4];
@@ -357,20 +360,20 @@ __global__ __launch_bounds__(kBlock) void stream_mix_ckpt_kernel(
     }
 }
 
-// Backward.  One wave per token at a time (grid-stride); a lane accumulates
-// its chunks' contribution to grad_H in 16 registers, the wave reduces them
-// once per token.
-template <int FMT>
+// Backward.  W = 64: one wave per token at a time (grid-stride); a lane
+// accumulates its chunks' contribution to grad_H in 16 registers, the wave
+// reduces them once per token.  W = 16, for narrow rows: 16 lanes per token.
+template <int FMT, int W>
 __global__ __launch_bounds__(kBlock) void stream_mix_bwd_ckpt_kernel(
     const uint2* __restrict__ codes, const uint8_t* __restrict__ scales,
     const float* __restrict__ H, const uint4* __restrict__ gout, uint4* __restrict__ gx,
     float* __restrict__ gH, int64_t T, int64_t C8)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t wave = (int64_t)blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
-    const int64_t nwaves = (int64_t)gridDim.x * (kBlock / 64);
+    const int lane = threadIdx.x & (W - 1);
+    const int64_t first = (int64_t)blockIdx.x * (kBlock / W) + threadIdx.x / W;
+    const int64_t step = (int64_t)gridDim.x * (kBlock / W);
     const int64_t Cb = (C8 + 3) / 4;
-    for (int64_t t = wave; t < T; t += nwaves) {
+    for (int64_t t = first; t < T; t += step) {
         float Mt[16];  // H transposed: grad_x_j = sum_i H_ij g_i
         const float4* hp = reinterpret_cast<const float4*>(H + 16 * t);
 #pragma unroll
@@ -385,7 +388,7 @@ __global__ __launch_bounds__(kBlock) void stream_mix_bwd_ckpt_kernel(
 #pragma unroll
         for (int k = 0; k < 16; ++k) acc[k] = 0.f;
         const int64_t row = t * 4;
-        for (int64_t c = lane; c < C8; c += 64) {
+        for (int64_t c = lane; c < C8; c += W) {
             uint4 gin[4], oo[4];
             uint2 q[4];
             uint32_t s[4];
@@ -412,8 +415,13 @@ __global__ __launch_bounds__(kBlock) void stream_mix_bwd_ckpt_kernel(
                         acc[4 * i + j] = __builtin_fmaf(gf[i][e], xf[e], acc[4 * i + j]);
             }
         }
-        const float sum = wave_sum_halving<16>(acc);
-        if ((lane & 3) == 0) gH[16 * t + (lane >> 2)] = sum;
+        if (W == 64) {
+            const float sum = wave_sum_halving<16>(acc);
+            if ((lane & 3) == 0) gH[16 * t + (lane >> 2)] = sum;
+        } else {
+            sum16_halving<16>(acc);
+            gH[16 * t + lane] = acc[0];
+        }
     }
 }
 
@@ -462,23 +470,40 @@ hipError_t unpack_as(const Packed& in, void* x, const Chunks& k, hipStream_t str
     return hipGetLastError();
 }
 
-template <int FMT>
+template <int FMT, bool NARROW>
 void mix_ckpt_as(const void* x, const float* Hl, float* H_out, void* out, const Packed& ckpt,
-                 int64_t T, int64_t C, const SolverOpts* proj, hipStream_t stream)
+                 int64_t T, int64_t C, int shift, const SolverOpts* proj, hipStream_t stream)
 {
     const dim3 grid(token_grid(T));
     const uint4* xv = static_cast<const uint4*>(x);
     uint4* ov = static_cast<uint4*>(out);
     uint2* cv = static_cast<uint2*>(ckpt.codes);
     if (proj == nullptr)
-        hipLaunchKernelGGL((stream_mix_ckpt_kernel<0, FMT>), grid, dim3(kBlock), 0, stream, xv, Hl,
-                           nullptr, ov, cv, ckpt.scales, T, C / 8, SolverOpts{});
+        hipLaunchKernelGGL((stream_mix_ckpt_kernel<0, FMT, NARROW>), grid, dim3(kBlock), 0, stream,
+                           xv, Hl, nullptr, ov, cv, ckpt.scales, T, C / 8, shift, SolverOpts{});
     else if (proj->solver == 0)
-        hipLaunchKernelGGL((stream_mix_ckpt_kernel<1, FMT>), grid, dim3(kBlock), 0, stream, xv, Hl,
-                           H_out, ov, cv, ckpt.scales, T, C / 8, *proj);
+        hipLaunchKernelGGL((stream_mix_ckpt_kernel<1, FMT, NARROW>), grid, dim3(kBlock), 0, stream,
+                           xv, Hl, H_out, ov, cv, ckpt.scales, T, C / 8, shift, *proj);
     else
-        hipLaunchKernelGGL((stream_mix_ckpt_kernel<2, FMT>), grid, dim3(kBlock), 0, stream, xv, Hl,
-                           H_out, ov, cv, ckpt.scales, T, C / 8, *proj);
+        hipLaunchKernelGGL((stream_mix_ckpt_kernel<2, FMT, NARROW>), grid, dim3(kBlock), 0, stream,
+                           xv, Hl, H_out, ov, cv, ckpt.scales, T, C / 8, shift, *proj);
+}
+
+template <int FMT>
+void mix_bwd_ckpt_as(const Packed& ckpt, const float* H, const void* gout, void* gx, float* gH,
+                     int64_t T, int64_t C, hipStream_t stream)
+{
+    const bool narrow = C <= 256;
+    const int64_t waves = narrow ? (T + 3) / 4 : T, most = waves < 8192 ? waves : 8192;
+    const dim3 grid((unsigned)((most + 3) / 4));
+    const uint2* cv = static_cast<const uint2*>(ckpt.codes);
+    const uint4* gv = static_cast<const uint4*>(gout);
+    if (narrow)
+        hipLaunchKernelGGL((stream_mix_bwd_ckpt_kernel<FMT, 16>), grid, dim3(kBlock), 0, stream, cv,
+                           ckpt.scales, H, gv, static_cast<uint4*>(gx), gH, T, C / 8);
+    else
+        hipLaunchKernelGGL((stream_mix_bwd_ckpt_kernel<FMT, 64>), grid, dim3(kBlock), 0, stream, cv,
+                           ckpt.scales, H, gv, static_cast<uint4*>(gx), gH, T, C / 8);
 }
 
 }  // namespace
@@ -544,10 +569,10 @@ hipError_t launch_stream_mix_ckpt(const void* x, const float* Hl, float* H_out, 
                                   const Packed& ckpt, int64_t T, int64_t C, int fmt,
                                   const SolverOpts* proj, hipStream_t stream)
 {
-    if (fmt == kE4M3)
-        mix_ckpt_as<kE4M3>(x, Hl, H_out, out, ckpt, T, C, proj, stream);
-    else
-        mix_ckpt_as<kInt8>(x, Hl, H_out, out, ckpt, T, C, proj, stream);
+    const int shift = token_shift((C + 31) / 32 * 4);
+    auto* f = fmt == kE4M3 ? (shift < 6 ? mix_ckpt_as<kE4M3, true> : mix_ckpt_as<kE4M3, false>)
+                           : (shift < 6 ? mix_ckpt_as<kInt8, true> : mix_ckpt_as<kInt8, false>);
+    f(x, Hl, H_out, out, ckpt, T, C, shift, proj, stream);
     return hipGetLastError();
 }
 
@@ -555,16 +580,10 @@ hipError_t launch_stream_mix_bwd_ckpt(const Packed& ckpt, const float* H, const 
                                       void* gx, float* gH, int64_t T, int64_t C, int fmt,
                                       hipStream_t stream)
 {
-    const int64_t waves_wanted = T < 8192 ? T : 8192;
-    const dim3 grid((unsigned)((waves_wanted + 3) / 4));
-    const uint2* cv = static_cast<const uint2*>(ckpt.codes);
-    const uint4* gv = static_cast<const uint4*>(gout);
     if (fmt == kE4M3)
-        hipLaunchKernelGGL(stream_mix_bwd_ckpt_kernel<kE4M3>, grid, dim3(kBlock), 0, stream, cv,
-                           ckpt.scales, H, gv, static_cast<uint4*>(gx), gH, T, C / 8);
+        mix_bwd_ckpt_as<kE4M3>(ckpt, H, gout, gx, gH, T, C, stream);
     else
-        hipLaunchKernelGGL(stream_mix_bwd_ckpt_kernel<kInt8>, grid, dim3(kBlock), 0, stream, cv,
-                           ckpt.scales, H, gv, static_cast<uint4*>(gx), gH, T, C / 8);
+        mix_bwd_ckpt_as<kInt8>(ckpt, H, gout, gx, gH, T, C, stream);
     return hipGetLastError();
 }
 

@@ -85,16 +85,17 @@ MHC_DEV int64_t dl_at(int64_t t, int part, int map)
 // ---------------------------------------------------------------------------
 // mix: read-mix u, write-back x_out and the checkpoints of x and f, 16 tokens
 // per workgroup (spaced by the grid size, so the workgroups stream a
-// contiguous front).
+// contiguous front), 2^shift threads to a token.
 // ---------------------------------------------------------------------------
 constexpr int kMixTokens = 16;
 
-template <int FMT>
+template <int FMT, bool NARROW>
 __global__ __launch_bounds__(kBlock) void layer_mix_ckpt_kernel(
     const uint4* __restrict__ x, const uint4* __restrict__ f, const float* __restrict__ Hpre,
     const float* __restrict__ Hpost, const float* __restrict__ Hres, uint4* __restrict__ u,
     uint4* __restrict__ xo, uint2* __restrict__ xc, uint8_t* __restrict__ xs_out,
-    uint2* __restrict__ fc, uint8_t* __restrict__ fs_out, int64_t T, int64_t C8)
+    uint2* __restrict__ fc, uint8_t* __restrict__ fs_out, int64_t T, int64_t C8,
+    int shift)
 {
     __shared__ float sM[kMixTokens][kMaps];
     const int64_t b = blockIdx.x, G = gridDim.x;
@@ -107,13 +108,13 @@ __global__ __launch_bounds__(kBlock) void layer_mix_ckpt_kernel(
         sM[tl][m] = m < 4 ? Hpre[4 * t + m] : (m < 8 ? Hpost[4 * t + m - 4] : Hres[16 * t + m - 8]);
     }
     __syncthreads();
-    for (int tl = 0; tl < nt; ++tl) {
+    for (int tl = first_token<NARROW>(tid, shift); tl < nt; tl += kBlock >> shift) {
         float M[kMaps];
 #pragma unroll
         for (int m = 0; m < kMaps; ++m) M[m] = sM[tl][m];
         const int64_t t = b + G * tl;
         // C8 is a multiple of 8: a quad of lanes (one block) is whole
-        for (int64_t c = tid; c < C8; c += kBlock) {
+        for (int64_t c = tid & ((1 << shift) - 1); c < C8; c += 1 << shift) {
             uint4 xq[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) xq[j] = mhc_load_stream(&x[(t * 4 + j) * C8 + c]);
@@ -165,7 +166,8 @@ __global__ __launch_bounds__(kBlock) void layer_mix_ckpt_kernel(
 // pipeline: step i+1's loads are issued into the other register set before
 // step i is consumed (the vector-memory counter retires in order), across
 // token boundaries too.  At a token's last chunk the 24 partial dots are
-// wave-reduced into LDS; then lanes 0..tw-1 each finish one token.
+// wave-reduced into LDS; then lanes 0..tw-1 each finish one token.  Narrow
+// rows (W = 16): 16 lanes to a token, four tokens at a time.
 // ---------------------------------------------------------------------------
 struct DotsLoads {
     uint2 x[4], f;
@@ -181,7 +183,7 @@ struct DotsLane {
     const uint4* gxo;
     const uint4* gu;
     int64_t T, C8, tb;
-    int nch, lane;
+    int nch, lane;  // chunks of W lanes in a row
 };
 
 // Place in a wave's sequence of steps: token tl, chunk ci of it.
@@ -195,12 +197,19 @@ MHC_DEV DotsStep dots_next(const DotsStep& s, int nch)
     return DotsStep{last ? s.tl + 1 : s.tl, last ? 0 : s.ci + 1};
 }
 
+template <int W>
+MHC_DEV int64_t dots_token(const DotsLane& L, const DotsStep& s)
+{
+    return W == 64 ? L.tb + s.tl : L.tb + (int64_t)(64 / W) * s.tl + L.lane / W;
+}
+
+template <int W>
 MHC_DEV void dots_issue(const DotsLane& L, DotsLoads& d, const DotsStep& s)
 {
     // steps past the wave's last one read clamped addresses and are never consumed
-    int64_t t = L.tb + s.tl;
+    int64_t t = dots_token<W>(L, s);
     t = t < L.T ? t : L.T - 1;
-    int64_t c = L.lane + 64 * (int64_t)s.ci;
+    int64_t c = (L.lane & (W - 1)) + W * (int64_t)s.ci;
     c = c < L.C8 ? c : L.C8 - 1;
     const int64_t cb = L.C8 / 4, b = c >> 2;
 #pragma unroll
@@ -214,12 +223,12 @@ MHC_DEV void dots_issue(const DotsLane& L, DotsLoads& d, const DotsStep& s)
     d.u = L.gu[t * L.C8 + c];
 }
 
-template <int FMT>
+template <int FMT, int W>
 MHC_DEV void dots_consume(const DotsLane& L, const DotsLoads& d, const DotsStep& s, float (&acc)[32],
                           float (*sDots)[kMaps])
 {
-    const int64_t t = L.tb + s.tl;
-    const int64_t c = L.lane + 64 * (int64_t)s.ci;
+    const int64_t t = dots_token<W>(L, s);
+    const int64_t c = (L.lane & (W - 1)) + W * (int64_t)s.ci;
     if (t < L.T && c < L.C8) {
         float sc[4];
 #pragma unroll
@@ -258,9 +267,19 @@ MHC_DEV void dots_consume(const DotsLane& L, const DotsLoads& d, const DotsStep&
         }
     }
     if (s.ci == L.nch - 1) {  // the token's last chunk: reduce its dots
-        const float sm = wave_sum_halving<32>(acc);
-        const int idx = (L.lane >> 1) & 31;
-        if ((L.lane & 1) == 0 && idx < kMaps) sDots[s.tl][idx] = sm;
+        if (W == 64) {
+            const float sm = wave_sum_halving<32>(acc);
+            const int idx = (L.lane >> 1) & 31;
+            if ((L.lane & 1) == 0 && idx < kMaps) sDots[s.tl][idx] = sm;
+        } else {
+            sum16_halving<32>(acc);
+            const int idx = 2 * (L.lane & 15);
+            if (idx < kMaps) {
+                float* d = sDots[(64 / W) * s.tl + L.lane / W];
+                d[idx] = acc[0];
+                d[idx + 1] = acc[1];
+            }
+        }
 #pragma unroll
         for (int k = 0; k < 32; ++k) acc[k] = 0.f;
     }
@@ -335,7 +354,7 @@ MHC_DEV void finish_token(const DotsOut& o, int64_t t, const float* dots)
     }
 }
 
-template <int FMT>
+template <int FMT, int W>
 __global__ __launch_bounds__(kBlock) void layer_dots_ckpt_kernel(
     const uint2* __restrict__ xc, const uint8_t* __restrict__ xs, const uint2* __restrict__ fc,
     const uint8_t* __restrict__ fs, const uint4* __restrict__ gxo, const uint4* __restrict__ gu,
@@ -347,23 +366,24 @@ __global__ __launch_bounds__(kBlock) void layer_dots_ckpt_kernel(
     const int64_t tb = ((int64_t)blockIdx.x * 4 + w) * tw;
     DotsLane L;
     L.xc = xc; L.xs = xs; L.fc = fc; L.fs = fs; L.gxo = gxo; L.gu = gu;
-    L.T = T; L.C8 = C8; L.nch = (int)((C8 + 63) / 64); L.tb = tb; L.lane = lane;
+    L.T = T; L.C8 = C8; L.nch = (int)((C8 + W - 1) / W); L.tb = tb; L.lane = lane;
     float acc[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-    // the steps are taken in pairs; an odd last one has tl = tw and does nothing
+    // the steps are taken in pairs; an odd last one is past the wave's tokens and does nothing
     DotsLoads d0, d1;
     DotsStep s0{0, 0};
-    dots_issue(L, d0, s0);
-    while (s0.tl < tw) {
+    dots_issue<W>(L, d0, s0);
+    const int n = tw / (64 / W);
+    while (s0.tl < n) {
         const DotsStep s1 = dots_next(s0, L.nch), s2 = dots_next(s1, L.nch);
-        dots_issue(L, d1, s1);
+        dots_issue<W>(L, d1, s1);
         __builtin_amdgcn_sched_barrier(0);
-        dots_consume<FMT>(L, d0, s0, acc, sDots[w]);
+        dots_consume<FMT, W>(L, d0, s0, acc, sDots[w]);
         __builtin_amdgcn_sched_barrier(0);
-        dots_issue(L, d0, s2);
+        dots_issue<W>(L, d0, s2);
         __builtin_amdgcn_sched_barrier(0);
-        if (s1.tl < tw) dots_consume<FMT>(L, d1, s1, acc, sDots[w]);
+        if (s1.tl < n) dots_consume<FMT, W>(L, d1, s1, acc, sDots[w]);
         __builtin_amdgcn_sched_barrier(0);
         s0 = s2;
     }
@@ -397,16 +417,16 @@ __global__ __launch_bounds__(kBlock) void layer_dots_few_ckpt_kernel(
         L.nch = nch + 1;  // no chunk is "the last": the reduction is here
         DotsLoads d0, d1;
         DotsStep s0{0, w};
-        dots_issue(L, d0, s0);
+        dots_issue<64>(L, d0, s0);
         while (s0.ci < nch) {
             const DotsStep s1{0, s0.ci + 4}, s2{0, s0.ci + 8};
-            dots_issue(L, d1, s1);
+            dots_issue<64>(L, d1, s1);
             __builtin_amdgcn_sched_barrier(0);
-            dots_consume<FMT>(L, d0, s0, acc, nullptr);
+            dots_consume<FMT, 64>(L, d0, s0, acc, nullptr);
             __builtin_amdgcn_sched_barrier(0);
-            dots_issue(L, d0, s2);
+            dots_issue<64>(L, d0, s2);
             __builtin_amdgcn_sched_barrier(0);
-            if (s1.ci < nch) dots_consume<FMT>(L, d1, s1, acc, nullptr);
+            if (s1.ci < nch) dots_consume<FMT, 64>(L, d1, s1, acc, nullptr);
             __builtin_amdgcn_sched_barrier(0);
             s0 = s2;
         }
@@ -767,9 +787,14 @@ hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, in
                            xc, x.scales, fc, f.scales, gxo, gu, o, C / 8);
     } else {
         int tw = 16;  // tokens per wave: a workgroup for every compute unit where there are as many tokens
-        while (tw > 1 && p.Tp / (4 * tw) < 256) tw /= 2;
-        hipLaunchKernelGGL(layer_dots_ckpt_kernel<FMT>, dim3((unsigned)(p.Tp / (4 * tw))), dim3(kBlock), 0,
-                           stream, xc, x.scales, fc, f.scales, gxo, gu, o, p.Tp, C / 8, tw);
+        while (tw > (C <= 256 ? 4 : 1) && p.Tp / (4 * tw) < 256) tw /= 2;
+        const dim3 grid((unsigned)(p.Tp / (4 * tw)));
+        if (C <= 256)
+            hipLaunchKernelGGL((layer_dots_ckpt_kernel<FMT, 16>), grid, dim3(kBlock), 0, stream, xc,
+                               x.scales, fc, f.scales, gxo, gu, o, p.Tp, C / 8, tw);
+        else
+            hipLaunchKernelGGL((layer_dots_ckpt_kernel<FMT, 64>), grid, dim3(kBlock), 0, stream, xc,
+                               x.scales, fc, f.scales, gxo, gu, o, p.Tp, C / 8, tw);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -798,10 +823,11 @@ template <int FMT>
 hipError_t layer_mix_as(const LayerPtrs& a, const Packed& x, const Packed& f, int64_t T, int64_t C,
                         hipStream_t stream)
 {
-    hipLaunchKernelGGL(layer_mix_ckpt_kernel<FMT>, dim3(token_grid(T)),
-                       dim3(kBlock), 0, stream, (const uint4*)a.x, (const uint4*)a.f, a.H_pre,
-                       a.H_post, a.H_res, (uint4*)a.u, (uint4*)a.x_out, (uint2*)x.codes, x.scales,
-                       (uint2*)f.codes, f.scales, T, C / 8);
+    const int shift = token_shift(C / 8);
+    auto* kernel = shift < 6 ? layer_mix_ckpt_kernel<FMT, true> : layer_mix_ckpt_kernel<FMT, false>;
+    hipLaunchKernelGGL(kernel, dim3(token_grid(T)), dim3(kBlock), 0, stream, (const uint4*)a.x,
+                       (const uint4*)a.f, a.H_pre, a.H_post, a.H_res, (uint4*)a.u, (uint4*)a.x_out,
+                       (uint2*)x.codes, x.scales, (uint2*)f.codes, f.scales, T, C / 8, shift);
     return hipGetLastError();
 }
 

@@ -19,6 +19,7 @@
 #pragma once
 
 #include "devmath.h"
+#include "wave.h"
 
 namespace mhc {
 
@@ -278,6 +279,35 @@ MHC_DEV void mx_store_stream(uint2* p, const uint2& q)
 {
     const mx_u32x2 v = {q.x, q.y};
     __builtin_nontemporal_store(v, reinterpret_cast<mx_u32x2*>(p));
+}
+
+// Sums over each 16 lanes of a wave of N = 16 or 32 partials: lane l holds
+// those of partials (N / 16) (l % 16) + 0 .. N / 16 - 1 in v[0 .. N / 16 - 1].
+template <int N>
+MHC_DEV void sum16_halving(float* v)
+{
+    halve_dpp<kDppBit3, 3, N / 2>(v);
+    halve_dpp<kDppBit2, 2, N / 4>(v);
+    halve_dpp<kDppBit1, 1, N / 8>(v);
+    halve_dpp<kDppBit0, 0, N / 16>(v);
+}
+
+// A token's place for a thread of a workgroup in which 2^shift share a token.
+// From 64 on a wave is within one token, whose rows then have scalar bases;
+// below that, NARROW kernels keep the addresses per lane.
+template <bool NARROW>
+MHC_DEV int first_token(int tid, int shift)
+{
+    return NARROW ? tid >> shift : __builtin_amdgcn_readfirstlane(tid >> shift);
+}
+
+// log2 of the threads of a workgroup that share a token of `chunks` chunks:
+// the fewest that take the row in one go, at least a quad (a block).
+inline int token_shift(int64_t chunks)
+{
+    int shift = 2;
+    while (shift < 8 && (1 << shift) < chunks) ++shift;
+    return shift;
 }
 
 }  // namespace mhc

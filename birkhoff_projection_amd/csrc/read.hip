@@ -63,19 +63,21 @@ MHC_DEV void store_u(const UOut& o, int64_t i, const float (&M)[4], const uint4 
 // u for many tokens: 16 tokens per workgroup, spaced by the grid size.
 constexpr int kMixTokens = 16;
 
+template <bool NARROW>
 __global__ __launch_bounds__(kBlock) void read_mix_kernel(const uint4* __restrict__ x,
                                                           const float* __restrict__ Hpre, UOut o,
-                                                          int64_t T, int64_t C8)
+                                                          int64_t T, int64_t C8, int shift)
 {
     const int64_t b = blockIdx.x, G = gridDim.x;
     const int tid = threadIdx.x;
-    for (int tl = 0; tl < kMixTokens; ++tl) {
+    // 2^shift threads share a token
+    for (int tl = first_token<NARROW>(tid, shift); tl < kMixTokens; tl += kBlock >> shift) {
         const int64_t t = b + G * tl;
         if (t >= T) return;
         const float4 h = reinterpret_cast<const float4*>(Hpre)[t];
         const float M[4] = {h.x, h.y, h.z, h.w};
         // C8 is a multiple of 8: a quad of lanes (one block) is whole
-        for (int64_t c = tid; c < C8; c += kBlock) {
+        for (int64_t c = tid & ((1 << shift) - 1); c < C8; c += 1 << shift) {
             uint4 xq[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) xq[j] = mhc_load_stream(&x[(t * 4 + j) * C8 + c]);
@@ -268,8 +270,10 @@ hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, in
     if (p.splits != 0) return launch_split(a, p, uo, T, C, eps, o, stream);
     const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(read_mix_kernel, dim3(token_grid(T)), dim3(kBlock), 0, stream,
-                       (const uint4*)a.x, a.H_pre, uo, T, C / 8);
+    const int shift = token_shift(C / 8);
+    auto* kernel = shift < 6 ? read_mix_kernel<true> : read_mix_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3(token_grid(T)), dim3(kBlock), 0, stream, (const uint4*)a.x,
+                       a.H_pre, uo, T, C / 8, shift);
     return hipGetLastError();
 }
 

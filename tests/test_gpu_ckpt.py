@@ -269,7 +269,7 @@ def check_layer_bwd(bw, fwd, xh, W64, fh, g64, u64):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("T,C", [(1, 64), (37, 64), (64, 128), (130, 192), (300, 576), (2048, 256), (1, 7168), (5, 1088), (66, 2624),
+@pytest.mark.parametrize("T,C", [(1, 64), (37, 64), (64, 128), (130, 192), (300, 576), (2048, 256), (1, 7168), (5, 1088), (66, 2624), (70, 448),
                                  (2049, 576), (2100, 64)])
 def test_layer_ckpt(gpu_lib, T, C, fmt):
     print(f"layer ckpt T={T} C={C} {fmt}", flush=True)
