@@ -113,10 +113,12 @@ MHC_DEV void store8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 // into the freed buffer, between that step's products.  The barrier waits for
 // the next stage's copies only (the counter retires in order).
 //
-// TAIL: K is no multiple of 64 KS.  Blocks past K are zeroed in A and get a
-// scale of 1.  Rows of scales may then start at any byte: the aligned words
-// around a row's bytes are copied, one more than it has, and a lane shifts its
-// bytes out of two of them.
+// TAIL: K is no multiple of 64 KS.  The last stage's pieces past K repeat the
+// row's last piece; scale bytes of 0 in both operands make them 2^-254 times
+// their product of at most 32 * 36, which is nothing to a sum in 32 bits.
+// Rows of scales may then start at any byte: the aligned words around a row's
+// bytes are copied, one more than it has, and a lane shifts its bytes out of
+// two of them.
 // ---------------------------------------------------------------------------
 
 // One copy of 16 (or 4) bytes per lane from global memory straight to LDS:
@@ -148,15 +150,14 @@ MHC_DEV int piece_at(int r, int c)
     return KS == 4 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
 }
 
-template <int KS, int S, bool TAIL, int TM, int TN>
+template <int KS, int S, int TM, int TN>
 MHC_DEV void read_frags(Frags<TM, TN>& f, const uint8_t* sA, const uint8_t* sB, int ra, int rb,
-                        int kh, int64_t left)
+                        int kh)
 {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int r = ra + 32 * i;
         f.a[i] = *reinterpret_cast<const uint4*>(sA + r * 32 * KS + 16 * piece_at<KS>(r, 2 * S + kh));
-        if (TAIL && left <= 2 * S) f.a[i] = make_uint4(0, 0, 0, 0);  // a block past K
     }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
@@ -267,19 +268,26 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
         rowX[i] = first;
     }
     // byte of its first word where a lane's scales begin (the same for all its
-    // rows: they are 32 apart), plus its block half
-    const int sa = (TAIL ? (int)(((m0 + ra) * Ks) & 3) : 0) + kh;
-    const int sb = (TAIL ? (int)(((n0 + rb) * Ks) & 3) : 0) + kh;
+    // rows: they are 32 apart)
+    const uint32_t sa = TAIL ? (uint32_t)((m0 + ra) * Ks) & 3 : 0;
+    const uint32_t sb = TAIL ? (uint32_t)((n0 + rb) * Ks) & 3 : 0;
+    // TAIL, last stage: bytes a thread's piece is past the row, and the lane's
+    // scale bytes (0 and 2 of each word) that exist
+    uint32_t cutLast = 0, maskLast[kWords];
+    if (TAIL) {
+        const int64_t over = (int64_t)(stages - 1) * kRowBytes + c16 - (Kb - 16);
+        cutLast = over > 0 ? (uint32_t)over : 0u;
+        const int64_t left = Ks - kRowBlocks * (int64_t)(stages - 1) - kh;
+#pragma unroll
+        for (int q = 0; q < kWords; ++q)
+            maskLast[q] = (left > 4 * q ? 0xffu : 0u) | (left > 4 * q + 2 ? 0xff0000u : 0u);
+    }
     const uint32_t ldsC = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sC[0][0];
     const uint32_t ldsX = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint32_t*)&sX[0][0];
     constexpr int NC = NA + NB + kCopied * NX;      // copies per thread and stage
     const auto copy = [&](int st, int buf, int i) {  // copy i of stage st
         if (i < NA + NB) {
-            uint32_t cut = 0;
-            if (TAIL) {  // bytes past the row repeat its last piece
-                const int64_t over = (int64_t)st * kRowBytes + c16 - (Kb - 16);
-                cut = over > 0 ? (uint32_t)over : 0u;
-            }
+            const uint32_t cut = TAIL && st == stages - 1 ? cutLast : 0u;
             const bool isA = i < NA;
             const uint8_t* base = (isA ? baseA : baseB) + (int64_t)st * kRowBytes;
             copy16_to_lds(base, (isA ? offA[isA ? i : 0] : offB[isA ? 0 : i - NA]) - cut,
@@ -305,22 +313,21 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
             for (int j = 0; j < TN; ++j) y.b[q][j] = sX[buf][q][BM + rb + 32 * j];
         }
     };
-    // the lane's own scales in bytes 0 and 2; `left` blocks exist
-    const auto shifted = [&](Scales<kWords, TM, TN>& x, const Scales<kCopied, TM, TN>& y, int64_t left) {
-        const auto pick = [&](uint32_t lo, uint32_t hi, int s, int q) {
-            if (!TAIL) return lo >> (8 * s);
-            uint32_t v = (uint32_t)((((uint64_t)hi << 32) | lo) >> (8 * s));
-            if (left <= 4 * q) v = 0x007f007fu;
-            else if (left <= 4 * q + 2) v = (v & 0xffu) | 0x007f0000u;
-            return v;
+    // the lane's own scales in bytes 0 and 2
+    const auto shifted = [&](Scales<kWords, TM, TN>& x, const Scales<kCopied, TM, TN>& y, int st) {
+        uint32_t mask = 0;
+        const auto pick = [&](uint32_t lo, uint32_t hi, uint32_t s) {
+            if (!TAIL) return lo >> (8 * kh);
+return (__builtin_amdgcn_alignbyte(hi, lo, s) >> (8 * kh)) & mask;
         };
 #pragma unroll
         for (int q = 0; q < kWords; ++q) {
             constexpr int one = TAIL ? 1 : 0;
+            if (TAIL) mask = st == stages - 1 ? maskLast[q] : 0xff00ffu;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) x.a[q][i] = pick(y.a[q][i], y.a[q + one][i], sa, q);
+            for (int i = 0; i < TM; ++i) x.a[q][i] = pick(y.a[q][i], y.a[q + one][i], sa);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) x.b[q][j] = pick(y.b[q][j], y.b[q + one][j], sb, q);
+            for (int j = 0; j < TN; ++j) x.b[q][j] = pick(y.b[q][j], y.b[q + one][j], sb);
         }
     };
     // next stage's copies landed, everybody's reads of this one done
@@ -346,26 +353,25 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
         for (int i = 0; i < NC; ++i) copy(clamped(b), b, i);
     }
     scales(y, 0);
-    shifted(x, y, Ks - kh);
-    read_frags<KS, 0, TAIL>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh, Ks - kh);
+    shifted(x, y, 0);
+    read_frags<KS, 0>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh);
     int buf = 0;
     for (int st = 0; st < stages; ++st) {
         const uint8_t* cA = sC[buf];
         const uint8_t* cB = cA + BM * kRowBytes;
         const int nxt = buf + 1 < NBUF ? buf + 1 : 0;
-        const int64_t left = Ks - kRowBlocks * (int64_t)st - kh;  // blocks from this lane's first one on
-        read_frags<KS, 1, TAIL>(f1, cA, cB, ra, rb, kh, left);
+        read_frags<KS, 1>(f1, cA, cB, ra, rb, kh);
         mma_step<0>(f0, x, acc);
         if constexpr (KS == 4) {
-            read_frags<KS, 2, TAIL>(f0, cA, cB, ra, rb, kh, left);
+            read_frags<KS, 2>(f0, cA, cB, ra, rb, kh);
             mma_step<1>(f1, x, acc);
-            read_frags<KS, 3, TAIL>(f1, cA, cB, ra, rb, kh, left);
+            read_frags<KS, 3>(f1, cA, cB, ra, rb, kh);
             mma_step<2>(f0, x, acc);
         }
         hand_over();
         const uint8_t* nA = sC[nxt];
         scales(y, nxt);
-        read_frags<KS, 0, TAIL>(f0, nA, nA + BM * kRowBytes, ra, rb, kh, left - kRowBlocks);
+        read_frags<KS, 0>(f0, nA, nA + BM * kRowBytes, ra, rb, kh);
         __builtin_amdgcn_sched_barrier(0);
         constexpr int kPer = (NC + TM * TN - 1) / (TM * TN);  // copies behind each product
 #pragma unroll
@@ -376,7 +382,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
             for (int i = kPer * q; i < kPer * (q + 1) && i < NC; ++i) copy(clamped(st + NBUF), buf, i);
             __builtin_amdgcn_sched_barrier(0);
         }
-        shifted(x, y, left - kRowBlocks);
+        shifted(x, y, st + 1);
         buf = nxt;
     }
     // every wave is done with the stage buffers before they hold the outputs
@@ -439,8 +445,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
 }
 
 // ---------------------------------------------------------------------------
-// Few rows of a (up to 16): bound by reading b once.  A workgroup takes 16
-// rows of b and all of a, K in panels of up to PT tiles of 256.  Waves 4..7
+// Few rows of a: bound by reading b once.  A workgroup takes 16 rows of b and
+// 16 of a (all of them, mostly), K in panels of up to PT tiles of 256.  Waves 4..7
 // copy the panel of b to LDS, every instruction 8 whole lines of 128 bytes;
 // meanwhile waves 0..3 put a there.  Then the 8 waves share the tiles; their
 // partial sums meet in LDS at the end and are added in wave order.
@@ -462,6 +468,7 @@ constexpr int kFewThreads = 64 * kFewWaves;
 
 struct FewShape {
     int MR, LR, PT;      // rows of a in LDS and their logarithm, tiles per panel
+    unsigned groups;     // of 16 rows of a
     unsigned lds;        // bytes
 };
 
@@ -474,8 +481,13 @@ __global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShap
     __shared__ float sR[kFewWaves][16][17];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int row = lane & 15, kq = lane >> 4;
-    const int M = (int)p.M, MR = sh.MR, PT = sh.PT;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    // workgroups b, b + 8, ... run on one die: there the row groups of a
+    // follow each other on the same rows of b
+    const unsigned q8 = blockIdx.x / 8;
+    const int64_t n0 = (int64_t)(q8 / sh.groups * 8 + blockIdx.x % 8) * 16;
+    const int64_t m0 = (int64_t)(q8 % sh.groups) * 16;
+    if (n0 >= p.N) return;
+    const int M = (int)(p.M - m0 < 16 ? p.M - m0 : 16), MR = sh.MR, PT = sh.PT;
     const int64_t Ks = p.K / 32, Kb = p.K / 2;
     const int tiles = (int)((p.K + 255) / 256);
     const bool words = (Ks & 3) == 0;  // scale rows are whole words
@@ -562,8 +574,8 @@ __global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShap
             copy_codes(p.b + n0 * Kb, 4, nB, t0, nt, sB, w - 4);
             copy_scales(p.bs + n0 * Ks, 4, nB, t0, nt, xB, w - 4);
         } else if constexpr (SRC == 0) {
-            copy_codes(p.a, sh.LR, M, t0, nt, sA, w);
-            copy_scales(p.as, sh.LR, M, t0, nt, xA, w);
+            copy_codes(p.a + m0 * Kb, sh.LR, M, t0, nt, sA, w);
+            copy_scales(p.as + m0 * Ks, sh.LR, M, t0, nt, xA, w);
         } else {
             for (int j = tid; j < total; j += 1024) {
                 if (j != tid) load_a(j);
@@ -615,7 +627,7 @@ __global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShap
     __syncthreads();
     // 8 columns per thread: 2 threads per row of a
     if (tid < 32) {
-        const int64_t m = tid >> 1, nn = n0 + 8 * (tid & 1);
+        const int64_t m = m0 + (tid >> 1), nn = n0 + 8 * (tid & 1);
         if (m < p.M && nn < p.N) {
             float y[8];
 #pragma unroll
@@ -647,7 +659,7 @@ void tile_as(const Mx4Args& p, hipStream_t stream)
     if (p.K % (64 * KS) == 0)
         hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, false>), dim3(gm * gn), block,
                            0, stream, p, gm, gn);
-    else if constexpr (WM * WN < 8)
+    else
         hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, true>), dim3(gm * gn), block,
                            0, stream, p, gm, gn);
 }
@@ -655,8 +667,8 @@ void tile_as(const Mx4Args& p, hipStream_t stream)
 // Panels sized for two workgroups per compute unit.
 FewShape few_shape(int64_t M, int64_t K)
 {
-    FewShape s{1, 0, 0, 0};
-    for (; s.MR < M; s.MR *= 2) ++s.LR;
+    FewShape s{1, 0, 0, (unsigned)((M + 15) / 16), 0};
+    for (; s.MR < 16 && s.MR < M; s.MR *= 2) ++s.LR;
     const int64_t tiles = (K + 255) / 256, most = 70 * 1024 / few_tile_bytes(s.MR);
     const int64_t panels = (tiles + most - 1) / most;
     s.PT = (int)((tiles + panels - 1) / panels);
@@ -668,8 +680,8 @@ template <int SRC, int EPI>
 void few_as(const Mx4Args& p, hipStream_t stream)
 {
     const FewShape sh = few_shape(p.M, p.K);
-    hipLaunchKernelGGL((mx4_few_kernel<SRC, EPI>), dim3((unsigned)((p.N + 15) / 16)), dim3(kFewThreads),
-                       sh.lds, stream, p, sh);
+    hipLaunchKernelGGL((mx4_few_kernel<SRC, EPI>), dim3((unsigned)((p.N + 127) / 128) * 8 * sh.groups),
+                       dim3(kFewThreads), sh.lds, stream, p, sh);
 }
 
 template <int EPI>
@@ -679,7 +691,12 @@ hipError_t matmul_as(const Mx4Args& p, int src, hipStream_t stream)
         few_as<1, EPI>(p, stream);
     } else if (src == 2) {
         few_as<2, EPI>(p, stream);
-    } else if (p.M <= 16) {
+    } else if (p.M <= 16 || (p.M + 15) / 16 * ((p.N + 15) / 16) <= 512) {
+        // As long as all workgroups of 16 x 16 are on the chip at once (two per
+        // compute unit) they beat the tiles below, which then leave most of it
+        // idle (us, against tiles of 64): 32 x 4096, K = 4096 5.5 / 7.4;
+        // 128 x 1024, K = 8192 7.7 / 13.5; but 64 x 4096 (1024 workgroups)
+        // 9.0 / 8.4 and 32 x 7168, K = 7168 (896) 13.2 / 11.2.
         few_as<0, EPI>(p, stream);
     } else {
         // Large tiles move the fewest operand bytes per product and win as
@@ -692,12 +709,8 @@ hipError_t matmul_as(const Mx4Args& p, int src, hipStream_t stream)
         // workgroup otherwise (4096 x 4096: 65 / 59).
         const int64_t t256 = ((p.M + 255) / 256) * ((p.N + 255) / 256);
         const int64_t t128 = ((p.M + 127) / 128) * ((p.N + 127) / 128);
-        // (8 waves are 3 % faster than 4 on the large tile, but with the tail's
-        // shifts they spill)
-        if (t256 >= 192 && p.K % 256 == 0)
+        if (t256 >= 192)
             tile_as<2, 4, 4, 2, 4, 2, EPI>(p, stream);
-        else if (t256 >= 192)
-            tile_as<4, 4, 2, 2, 4, 2, EPI>(p, stream);
         else if (t128 > 256)
             tile_as<2, 2, 2, 2, 4, 2, EPI>(p, stream);
         else if (t128 >= 128)
