@@ -14,7 +14,8 @@ from .ops import (BirkhoffProjection, birkhoff_bwd, birkhoff_bwd_n, birkhoff_bwd
                   stream_mix, stream_mix_bwd)
 from .packed import (Mx4Linear, ProjectedMix, ckpt_pack, ckpt_unpack, layer_bwd_ckpt,
                      layer_ckpt_workspace, layer_fwd_ckpt, layer_read, mx4_dequantize, mx4_linear,
-                     mx4_matmul, mx4_quantize, mx4_write_back, projected_mix, stream_mix_bwd_ckpt,
+                     mx4_matmul, mx4_quantize, mx4_quantize_both, mx4_quantize_ckpt, mx4_requantize,
+                     mx4_write_back, projected_mix, stream_mix_bwd_ckpt,
                      stream_mix_ckpt)
 
 __all__ = ["LIB_PATH", "MHCError", "lib", "BirkhoffProjection", "birkhoff_bwd",
@@ -24,5 +25,6 @@ __all__ = ["LIB_PATH", "MHCError", "lib", "BirkhoffProjection", "birkhoff_bwd",
            "make_opts", "stream_mix", "stream_mix_bwd",
            "Mx4Linear", "ProjectedMix", "ckpt_pack", "ckpt_unpack", "layer_bwd_ckpt",
            "layer_ckpt_workspace", "layer_fwd_ckpt", "layer_read", "mx4_dequantize", "mx4_linear",
-           "mx4_matmul", "mx4_quantize", "mx4_write_back", "projected_mix", "stream_mix_bwd_ckpt",
+           "mx4_matmul", "mx4_quantize", "mx4_quantize_both", "mx4_quantize_ckpt", "mx4_requantize",
+           "mx4_write_back", "projected_mix", "stream_mix_bwd_ckpt",
            "stream_mix_ckpt"]

@@ -81,6 +81,12 @@ SIGNATURES = {
                                      c_void_p]),
     "mhc_mx4_quantize": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64,
                                    c_int32, c_void_p]),
+    "mhc_mx4_quantize_both": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_int64, c_int64, c_void_p]),
+    "mhc_mx4_quantize_ckpt": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_int64, c_int64, c_int32, c_void_p]),
+    "mhc_mx4_requantize": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                                     c_int32, c_void_p]),
     "mhc_mx4_dequantize": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int64, c_int64,
                                      c_void_p]),
     "mhc_mx4_matmul": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int64,

@@ -751,6 +751,71 @@ mhc_status mhc_mx4_quantize(const void* x, int32_t dtype, void* codes, uint8_t* 
                     "mx4_quantize launch");
 }
 
+mhc_status mhc_mx4_quantize_both(const void* x, int32_t dtype, void* codes, uint8_t* scales,
+                                 void* t_codes, uint8_t* t_scales, int64_t R, int64_t C, void* stream)
+{
+    mhc_status s;
+    if ((s = check_dtype(dtype)) != MHC_OK || (s = check_matrix(R, C, 32)) != MHC_OK) return s;
+    if (R % 32 != 0)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "R must be a multiple of 32 (got %lld)", (long long)R);
+    if ((R + 255) / 256 * ((C + 63) / 64) > INT32_MAX)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "R=%lld out of range for C=%lld", (long long)R, (long long)C);
+    if (R == 0) return ok();
+    const size_t n = (size_t)R * (size_t)C;
+    const Buf b[] = {{x, n * dtype_bytes(dtype), "x"},
+                     {codes, n / 2, "codes"},
+                     {scales, n / 32, "scales"},
+                     {t_codes, n / 2, "t_codes"},
+                     {t_scales, n / 32, "t_scales"}};
+    if ((s = check_buffers(b, 5)) != MHC_OK) return s;
+    return launched(mhc::launch_mx4_quantize_both(x, dtype == MHC_FP32, mhc::Packed{codes, scales},
+                                                  mhc::Packed{t_codes, t_scales}, R, C, (hipStream_t)stream),
+                    "mx4_quantize_both launch");
+}
+
+mhc_status mhc_mx4_quantize_ckpt(const void* x, int32_t dtype, void* codes, uint8_t* scales,
+                                 void* ckpt_codes, uint8_t* ckpt_scales, int64_t R, int64_t C,
+                                 int32_t format, void* stream)
+{
+    mhc_status s;
+    if ((s = check_dtype(dtype)) != MHC_OK || (s = check_format(format)) != MHC_OK ||
+        (s = check_matrix(R, C, 32)) != MHC_OK)
+        return s;
+    if (R == 0) return ok();
+    const size_t n = (size_t)R * (size_t)C;
+    const Buf b[] = {{x, n * dtype_bytes(dtype), "x"},
+                     {codes, n / 2, "codes"},
+                     {scales, n / 32, "scales"},
+                     {ckpt_codes, n, "ckpt_codes"},
+                     {ckpt_scales, n / 32, "ckpt_scales"}};
+    if ((s = check_buffers(b, 5)) != MHC_OK) return s;
+    return launched(mhc::launch_mx4_quantize_ckpt(x, dtype == MHC_FP32, mhc::Packed{codes, scales},
+                                                  mhc::Packed{ckpt_codes, ckpt_scales}, R, C, format,
+                                                  (hipStream_t)stream),
+                    "mx4_quantize_ckpt launch");
+}
+
+mhc_status mhc_mx4_requantize(const void* ckpt_codes, const uint8_t* ckpt_scales, void* codes,
+                              uint8_t* scales, int64_t R, int64_t C, int32_t format, void* stream)
+{
+    mhc_status s;
+    if ((s = check_format(format)) != MHC_OK || (s = check_matrix(R, C, 32)) != MHC_OK) return s;
+    if (R % 32 != 0)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "R must be a multiple of 32 (got %lld)", (long long)R);
+    if (C > 128 * (int64_t)65535)
+        return fail(MHC_ERR_INVALID_ARGUMENT, "C=%lld out of range", (long long)C);
+    if (R == 0) return ok();
+    const size_t n = (size_t)R * (size_t)C;
+    const Buf b[] = {{ckpt_codes, n, "ckpt_codes"},
+                     {ckpt_scales, n / 32, "ckpt_scales"},
+                     {codes, n / 2, "codes"},
+                     {scales, n / 32, "scales"}};
+    if ((s = check_buffers(b, 4)) != MHC_OK) return s;
+    const mhc::Packed in{const_cast<void*>(ckpt_codes), const_cast<uint8_t*>(ckpt_scales)};
+    return launched(mhc::launch_mx4_requantize(in, mhc::Packed{codes, scales}, R, C, format, (hipStream_t)stream),
+                    "mx4_requantize launch");
+}
+
 mhc_status mhc_mx4_dequantize(const void* codes, const uint8_t* scales, void* x, int32_t dtype,
                               int64_t R, int64_t C, void* stream)
 {

@@ -366,6 +366,66 @@ std::tuple<int, Tensor, Tensor> mx4_quantize(const Tensor& x, bool transpose, co
     return {st, std::move(codes), std::move(scales)};
 }
 
+// [R, C] values to be packed along rows and columns alike
+void square_blocks(const Tensor& x, const char* name)
+{
+    TORCH_CHECK_VALUE(x.dim() == 2 && x.size(0) % kBlock == 0 && x.size(1) % kBlock == 0, name,
+                      " must be [R, C] with R and C multiples of ", kBlock, ", got ", x.sizes());
+}
+
+struct Pair {
+    Tensor codes, scales;
+};
+
+// a new 4-bit [R, C] matrix
+Pair new_mx4(const Tensor& like, int64_t R, int64_t C)
+{
+    const auto o = like.options().dtype(at::kByte);
+    return Pair{at::empty({R, C / 2}, o), at::empty({R, C / kBlock}, o)};
+}
+
+// codes, scales, transposed codes, transposed scales
+std::tuple<int, Tensor, Tensor, Tensor, Tensor> mx4_quantize_both(const Tensor& x)
+{
+    const int32_t dt = values(x, "x");
+    square_blocks(x, "x");
+    const int64_t R = x.size(0), C = x.size(1);
+    const c10::DeviceGuard guard(x.device());
+    Pair r = new_mx4(x, R, C), t = new_mx4(x, C, R);
+    const int st = mhc_mx4_quantize_both(x.const_data_ptr(), dt, r.codes.data_ptr(), u8_out(r.scales),
+                                         t.codes.data_ptr(), u8_out(t.scales), R, C, stream_of(x));
+    return {st, std::move(r.codes), std::move(r.scales), std::move(t.codes), std::move(t.scales)};
+}
+
+// codes, scales, checkpoint codes, checkpoint scales
+std::tuple<int, Tensor, Tensor, Tensor, Tensor> mx4_quantize_ckpt(const Tensor& x, int32_t format)
+{
+    const int32_t dt = values(x, "x");
+    TORCH_CHECK_VALUE(x.dim() == 2 && x.size(1) % kBlock == 0, "x must be [R, C] with C a multiple of ", kBlock,
+                      ", got ", x.sizes());
+    const int64_t R = x.size(0), C = x.size(1);
+    const c10::DeviceGuard guard(x.device());
+    Pair q = new_mx4(x, R, C);
+    Tensor codes = at::empty(x.sizes(), x.options().dtype(at::kByte));
+    Tensor scales = at::empty({R, C / kBlock}, x.options().dtype(at::kByte));
+    const int st = mhc_mx4_quantize_ckpt(x.const_data_ptr(), dt, q.codes.data_ptr(), u8_out(q.scales),
+                                         codes.data_ptr(), u8_out(scales), R, C, format, stream_of(x));
+    return {st, std::move(q.codes), std::move(q.scales), std::move(codes), std::move(scales)};
+}
+
+std::tuple<int, Tensor, Tensor> mx4_requantize(const Tensor& codes, const Tensor& scales, int32_t format)
+{
+    need(codes, "codes", at::kByte);
+    square_blocks(codes, "codes");
+    const int64_t R = codes.size(0), C = codes.size(1);
+    given(scales, "scales", at::kByte, {R, C / kBlock}, codes.device());
+    const c10::DeviceGuard guard(codes.device());
+    Pair t = new_mx4(codes, C, R);
+    const int st = mhc_mx4_requantize(codes.const_data_ptr(), u8(scales), t.codes.data_ptr(), u8_out(t.scales), R,
+                                      C, format, stream_of(codes));
+    return {st, std::move(t.codes), std::move(t.scales)};
+}
+
 struct Mx4 {
     const void* codes;
     const uint8_t* scales;
@@ -443,6 +503,49 @@ std::tuple<int, Tensor> mx4_write_back(const Tensor& ac, const Tensor& as, const
     return {st, std::move(y)};
 }
 
+// A linear map's forward: y = q(x) q(w)^T, and x as a checkpoint.  Returns y
+// and the checkpoint's codes and scales.
+std::tuple<int, Tensor, Tensor, Tensor> mx4_linear_fwd(const Tensor& x, const Tensor& w, int32_t format)
+{
+    auto [sx, xc, xs, codes, scales] = mx4_quantize_ckpt(x, format);
+    auto [sw, wc, ws] = mx4_quantize(w, false, Opt(), Opt());
+    int st = sx != MHC_OK ? sx : sw;
+    Tensor y;
+    if (st == MHC_OK) std::tie(st, y) = mx4_matmul(xc, xs, wc, ws, values(x, "x"), Opt());
+    return {st, std::move(y), std::move(codes), std::move(scales)};
+}
+
+// Its backward: grad_x = q(gy) q(w^T)^T and grad_w = q(gy^T) q(xhat^T)^T, each
+// if wanted; M > 0.
+std::tuple<int, Opt, Opt> mx4_linear_bwd(const Tensor& codes, const Tensor& scales, const Tensor& w,
+                                         const Tensor& gy, int32_t format, bool want_x, bool want_w)
+{
+    Opt gx, gw;
+    Pair r, t;
+    int st = MHC_OK;
+    if (want_x && want_w)
+        std::tie(st, r.codes, r.scales, t.codes, t.scales) = mx4_quantize_both(gy);
+    else if (want_x)
+        std::tie(st, r.codes, r.scales) = mx4_quantize(gy, false, Opt(), Opt());
+    else if (want_w)
+        std::tie(st, t.codes, t.scales) = mx4_quantize(gy, true, Opt(), Opt());
+    if (st == MHC_OK && want_x) {
+        Tensor y;
+        auto [sw, wc, ws] = mx4_quantize(w, true, Opt(), Opt());
+        st = sw;
+        if (st == MHC_OK) std::tie(st, y) = mx4_matmul(r.codes, r.scales, wc, ws, values(gy, "grad"), Opt());
+        gx = std::move(y);
+    }
+    if (st == MHC_OK && want_w) {
+        Tensor y;
+        auto [sx, xc, xs] = mx4_requantize(codes, scales, format);
+        st = sx;
+        if (st == MHC_OK) std::tie(st, y) = mx4_matmul(t.codes, t.scales, xc, xs, values(w, "w"), Opt());
+        gw = std::move(y);
+    }
+    return {st, std::move(gx), std::move(gw)};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_binding, m)
@@ -455,8 +558,13 @@ PYBIND11_MODULE(_binding, m)
     m.def("layer_bwd_ckpt", &layer_bwd_ckpt);
     m.def("layer_read", &layer_read);
     m.def("mx4_quantize", &mx4_quantize);
+    m.def("mx4_quantize_both", &mx4_quantize_both);
+    m.def("mx4_quantize_ckpt", &mx4_quantize_ckpt);
+    m.def("mx4_requantize", &mx4_requantize);
     m.def("mx4_dequantize", &mx4_dequantize);
     m.def("mx4_matmul", &mx4_matmul);
     m.def("mx4_matmul_values", &mx4_matmul_values);
     m.def("mx4_write_back", &mx4_write_back);
+    m.def("mx4_linear_fwd", &mx4_linear_fwd);
+    m.def("mx4_linear_bwd", &mx4_linear_bwd);
 }

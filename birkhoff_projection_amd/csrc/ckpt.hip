@@ -42,15 +42,18 @@ MHC_DEV bool chunk_of(int64_t row0, uint32_t q, uint32_t P8, uint32_t C8, int64_
 // ---------------------------------------------------------------------------
 // pack: a wave takes 256 chunks in 4 loads per lane, all issued first.  The
 // 64 scale bytes of a wave are gathered in LDS and leave as one 64-byte
-// store.
+// store.  AND4: an 8-bit pack that writes the 4-bit one as well.
 // ---------------------------------------------------------------------------
-template <int FMT, bool F32, bool RAG>
+template <int FMT, bool F32, bool RAG, bool AND4 = false>
 __global__ __launch_bounds__(kBlock) void pack_kernel(const uint4* __restrict__ x,
                                                       void* __restrict__ codes,
-                                                      uint8_t* __restrict__ scales, int64_t n,
+                                                      uint8_t* __restrict__ scales,
+                                                      uint32_t* __restrict__ codes4,
+                                                      uint8_t* __restrict__ scales4, int64_t n,
                                                       uint32_t P8, uint32_t C8)
 {
     __shared__ __attribute__((aligned(16))) uint8_t sS[kBlock / 64][kWaveChunks / 4];
+    __shared__ __attribute__((aligned(16))) uint8_t sS4[AND4 ? kBlock / 64 : 1][kWaveChunks / 4];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t base = ((int64_t)blockIdx.x * (kBlock / 64) + w) * kWaveChunks;
     if (base >= n) return;
@@ -93,6 +96,15 @@ __global__ __launch_bounds__(kBlock) void pack_kernel(const uint4* __restrict__ 
         }
         amax = mx_quad_max(amax);
         const uint32_t s = mx_scale_byte<FMT>(amax);
+        if constexpr (AND4) {
+            const uint32_t s4 = mx_scale_byte<kE2M1>(amax);
+            float f4[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f4[e] = F32 ? f[e] : 0.f;
+            const uint32_t c4 = F32 ? mx_encode8_e2m1(f4, amax, s4) : mx_encode8_e2m1(v[u][0], amax, s4);
+            if (in[u]) codes4[off[u]] = c4;
+            if ((lane & 3) == 0) sS4[w][16 * u + (lane >> 2)] = (uint8_t)s4;
+        }
         if (FMT == kE2M1) {
             const uint32_t c = F32 ? mx_encode8_e2m1(f, amax, s) : mx_encode8_e2m1(v[u][0], amax, s);
             if (in[u]) reinterpret_cast<uint32_t*>(codes)[off[u]] = c;
@@ -104,12 +116,16 @@ __global__ __launch_bounds__(kBlock) void pack_kernel(const uint4* __restrict__ 
         if ((lane & 3) == 0) sS[w][16 * u + (lane >> 2)] = (uint8_t)s;
     }
     mhc_wave_lds_fence();
-    uint8_t* dst = scales + base / 4;
-    if (base + kWaveChunks <= n) {
-        if (lane < 16) reinterpret_cast<uint32_t*>(dst)[lane] = *reinterpret_cast<const uint32_t*>(&sS[w][4 * lane]);
-    } else if (base + 4 * lane < n) {
-        dst[lane] = sS[w][lane];
-    }
+    const auto store_scales = [&](uint8_t* all, const uint8_t* from) {
+        uint8_t* dst = all + base / 4;
+        if (base + kWaveChunks <= n) {
+            if (lane < 16) reinterpret_cast<uint32_t*>(dst)[lane] = *reinterpret_cast<const uint32_t*>(&from[4 * lane]);
+        } else if (base + 4 * lane < n) {
+            dst[lane] = from[lane];
+        }
+    };
+    store_scales(scales, sS[w]);
+    if constexpr (AND4) store_scales(scales4, sS4[w]);
 }
 
 template <int FMT, bool F32, bool RAG>
@@ -166,86 +182,201 @@ __global__ __launch_bounds__(kBlock) void unpack_kernel(const void* __restrict__
 // takes 2 adjacent columns of 32 rows, so its two block maxima and all codes
 // stay in the lane, and each load instruction covers 64 columns of 2 rows.
 // The codes go through LDS so that a column's 128 bytes leave together.
+// ROWS: the rows are packed as well, from a copy of the tile in LDS; a lane
+// then takes 8 columns of a row, as in pack.  One read of x instead of two.
+// Tiles of one band of rows run one after the other on one die, so that the
+// 32 bytes of codes of each tile's row meet in its cache.
 // ---------------------------------------------------------------------------
 constexpr int kTrRows = 256, kTrCols = 64;
 constexpr int kTrPitch = kTrRows / 2 + 16;  // bytes per column of codes in LDS
 
-template <bool F32>
-__global__ __launch_bounds__(kBlock) void pack_transposed_kernel(
-    const void* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-    int64_t R, int64_t C)
+// 32 rows of two adjacent columns (bf16 pairs) to codes and scale bytes, the
+// second column's `pitch` and `spitch` bytes behind the first's.
+MHC_DEV void pack_column_pair(const uint32_t (&v)[32], uint8_t* codes, int pitch, uint8_t* scale, int spitch)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t sC[kTrCols][kTrPitch];
-    __shared__ __attribute__((aligned(8))) uint8_t sS[kTrCols][kTrRows / 32];
-    const int tid = threadIdx.x;
-    const int cp = tid & 31, rb = tid >> 5;   // column pair, row block of 32
-    const int64_t r0 = (int64_t)blockIdx.x * kTrRows, c0 = (int64_t)blockIdx.y * kTrCols;
-    const int64_t r = r0 + 32 * rb;
-    int64_t c = c0 + 2 * cp;
-    c = c < C ? c : C - 2;                    // columns past the end: loaded, not stored
-    if (r < R) {                              // R is a multiple of 32: a block is whole
-        uint32_t q[2][16];                    // per column: 16 packed pairs of rows
-        uint32_t amax[2] = {0, 0};
-        float f[2][F32 ? 32 : 1];
-        if (F32) {
-            const float* p = reinterpret_cast<const float*>(x) + r * C + c;
+    mx_u16x2 m = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float2 v = *reinterpret_cast<const float2*>(p + i * C);
-                f[0][F32 ? i : 0] = v.x;
-                f[1][F32 ? i : 0] = v.y;
-            }
+    for (int i = 0; i < 32; ++i)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(mx_u16x2, v[i] & 0x7fff7fffu));
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t amax = (uint32_t)(k ? m.y : m.x) << 16, sel = k ? 0x07060302u : 0x05040100u;
+        const uint32_t s = mx_scale_byte<kE2M1>(amax);
+        uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    const uint32_t m = mx_amax8(&f[k][F32 ? i : 0]);
-                    amax[k] = m > amax[k] ? m : amax[k];
-                }
-        } else {
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(x) + r * C + c;
-            uint32_t v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = *reinterpret_cast<const uint32_t*>(p + i * C);
-            mx_u16x2 m = {0, 0};
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                m = __builtin_elementwise_max(m, __builtin_bit_cast(mx_u16x2, v[i] & 0x7fff7fffu));
-            amax[0] = (uint32_t)m.x << 16;
-            amax[1] = (uint32_t)m.y << 16;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                q[0][i] = mx_perm(v[2 * i + 1], v[2 * i], 0x05040100u);
-                q[1][i] = mx_perm(v[2 * i + 1], v[2 * i], 0x07060302u);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t s = mx_scale_byte<kE2M1>(amax[k]);
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = F32 ? mx_encode8_e2m1(&f[k][F32 ? 8 * i : 0], amax[k], s)
-                           : mx_encode8_e2m1(make_uint4(q[k][4 * i], q[k][4 * i + 1], q[k][4 * i + 2],
-                                                        q[k][4 * i + 3]), amax[k], s);
-            *reinterpret_cast<uint4*>(&sC[2 * cp + k][16 * rb]) = make_uint4(o[0], o[1], o[2], o[3]);
-            sS[2 * cp + k][rb] = (uint8_t)s;
-        }
+        for (int i = 0; i < 4; ++i)
+            o[i] = mx_encode8_e2m1(make_uint4(mx_perm(v[8 * i + 1], v[8 * i], sel),
+                                              mx_perm(v[8 * i + 3], v[8 * i + 2], sel),
+                                              mx_perm(v[8 * i + 5], v[8 * i + 4], sel),
+                                              mx_perm(v[8 * i + 7], v[8 * i + 6], sel)), amax, s);
+        *reinterpret_cast<uint4*>(codes + k * pitch) = make_uint4(o[0], o[1], o[2], o[3]);
+        scale[k * spitch] = (uint8_t)s;
     }
-    __syncthreads();
+}
+
+// A tile's columns of codes and scales from LDS to memory.
+template <int COLS>
+MHC_DEV void store_columns(const uint8_t (*sC)[kTrPitch], const uint8_t (*sS)[kTrRows / 32],
+                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t r0,
+                           int64_t c0, int64_t R, int64_t C)
+{
+    const int tid = threadIdx.x;
     const int nb = (int)(R - r0 < kTrRows ? (R - r0) / 32 : kTrRows / 32);  // row blocks here
 #pragma unroll
-    for (int i = 0; i < kTrCols * 8 / kBlock; ++i) {
+    for (int i = 0; i < COLS * 8 / kBlock; ++i) {
         const int p = tid + kBlock * i, col = p >> 3, b = p & 7;
         if (c0 + col < C && b < nb)
             *reinterpret_cast<uint4*>(codes + (c0 + col) * (R / 2) + r0 / 2 + 16 * b) =
                 *reinterpret_cast<const uint4*>(&sC[col][16 * b]);
     }
 #pragma unroll
-    for (int i = 0; i < kTrCols * 8 / kBlock; ++i) {
+    for (int i = 0; i < COLS * 8 / kBlock; ++i) {
         const int p = tid + kBlock * i, col = p >> 3, b = p & 7;
         if (c0 + col < C && b < nb) scales[(c0 + col) * (R / 32) + r0 / 32 + b] = sS[col][b];
     }
+}
+
+template <bool F32, bool ROWS>
+__global__ __launch_bounds__(kBlock) void pack_transposed_kernel(
+    const void* __restrict__ x, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+    uint32_t* __restrict__ row_codes, uint8_t* __restrict__ row_scales, int64_t R, int64_t C)
+{
+    constexpr int kRowWords = kTrCols * (F32 ? 4 : 2) / 4;  // of the copy
+    __shared__ __attribute__((aligned(16))) uint8_t sC[kTrCols][kTrPitch];
+    __shared__ __attribute__((aligned(8))) uint8_t sS[kTrCols][kTrRows / 32];
+    __shared__ __attribute__((aligned(16))) uint32_t sV[ROWS ? kTrRows : 1][kRowWords];
+    const int tid = threadIdx.x;
+    const int cp = tid & 31, rb = tid >> 5;   // column pair, row block of 32
+    int64_t bx = blockIdx.x, by = blockIdx.y;
+    if (ROWS) {  // a linear grid: column tiles fastest, each die a run of tiles
+        const unsigned total = gridDim.x, per = total / 8, extra = total % 8, die = blockIdx.x % 8;
+        const unsigned t = die * per + (die < extra ? die : extra) + blockIdx.x / 8;
+        const unsigned gc = (unsigned)((C + kTrCols - 1) / kTrCols);
+        bx = t / gc;
+        by = t % gc;
+    }
+    const int64_t r0 = bx * kTrRows, c0 = by * kTrCols;
+    const int64_t r = r0 + 32 * rb;
+    int64_t c = c0 + 2 * cp;
+    c = c < C ? c : C - 2;                    // columns past the end: loaded, not stored
+    // row i of the tile is at row i ^ (i / 32 % 2) of the copy: a wave writes
+    // rows i and i + 32 at once, which so fall on different banks
+    if (r < R) {                              // R is a multiple of 32: a block is whole
+        if constexpr (F32) {
+            const float* p = reinterpret_cast<const float*>(x) + r * C + c;
+            float f[2][32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float2 v = *reinterpret_cast<const float2*>(p + i * C);
+                f[0][i] = v.x;
+                f[1][i] = v.y;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t amax = 0;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    const uint32_t m = mx_amax8(&f[k][i]);
+                    amax = m > amax ? m : amax;
+                }
+                if constexpr (ROWS)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        sV[32 * rb + (i ^ (rb & 1))][2 * cp + k] = __float_as_uint(f[k][i]);
+                const uint32_t s = mx_scale_byte<kE2M1>(amax);
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = mx_encode8_e2m1(&f[k][8 * i], amax, s);
+                *reinterpret_cast<uint4*>(&sC[2 * cp + k][16 * rb]) = make_uint4(o[0], o[1], o[2], o[3]);
+                sS[2 * cp + k][rb] = (uint8_t)s;
+            }
+        } else {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(x) + r * C + c;
+            uint32_t v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = *reinterpret_cast<const uint32_t*>(p + i * C);
+            if constexpr (ROWS)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sV[32 * rb + (i ^ (rb & 1))][cp] = v[i];
+            pack_column_pair(v, &sC[2 * cp][16 * rb], kTrPitch, &sS[2 * cp][rb], kTrRows / 32);
+        }
+    }
+    __syncthreads();
+    store_columns<kTrCols>(sC, sS, codes, scales, r0, c0, R, C);
+    if constexpr (ROWS) {
+        // 8 columns per lane; C is a multiple of 32 here, so a quad is whole
+#pragma unroll
+        for (int j = 0; j < kTrRows * 8 / kBlock; ++j) {
+            const int p = tid + kBlock * j, row = p >> 3, c8 = p & 7;
+            const int64_t rr = r0 + row, cc = c0 + 8 * c8;
+            const uint4* q = reinterpret_cast<const uint4*>(&sV[row ^ ((row >> 5) & 1)][kRowWords / 8 * c8]);
+            uint32_t amax, s, o;
+            if constexpr (F32) {
+                const float4 a = __builtin_bit_cast(float4, q[0]), b = __builtin_bit_cast(float4, q[1]);
+                float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                amax = mx_quad_max(mx_amax8(f));
+                s = mx_scale_byte<kE2M1>(amax);
+                o = mx_encode8_e2m1(f, amax, s);
+            } else {
+                const uint4 v = q[0];
+                amax = mx_quad_max(mx_amax8(v));
+                s = mx_scale_byte<kE2M1>(amax);
+                o = mx_encode8_e2m1(v, amax, s);
+            }
+            if (rr < R && cc < C) {
+                row_codes[(rr * C + cc) / 8] = o;
+                if ((c8 & 3) == 0) row_scales[(rr * C + cc) / 32] = (uint8_t)s;
+            }
+        }
+    }
+}
+
+// The same from an 8-bit checkpoint (C a multiple of 32): what unpacking it
+// and packing the transpose gives, without the values in between.  A workgroup
+// takes 256 rows x 128 columns, a lane 4 adjacent columns of 32 rows.
+constexpr int kReCols = 128;
+
+template <int FMT>
+__global__ __launch_bounds__(kBlock) void repack_transposed_kernel(
+    const uint8_t* __restrict__ ckpt, const uint8_t* __restrict__ ckpt_scales,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t R, int64_t C)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t sC[kReCols][kTrPitch];
+    __shared__ __attribute__((aligned(8))) uint8_t sS[kReCols][kTrRows / 32];
+    __shared__ __attribute__((aligned(4))) uint8_t sX[kTrRows][kReCols / 32];
+    const int tid = threadIdx.x;
+    const int cq = tid & 31, rb = tid >> 5;   // 4 columns, row block of 32
+    const int64_t r0 = (int64_t)blockIdx.x * kTrRows, c0 = (int64_t)blockIdx.y * kReCols;
+    const int64_t r = r0 + 32 * rb, Cb = C / 32;
+    int64_t c = c0 + 4 * cq;
+    c = c < C ? c : C - 4;                    // columns past the end: loaded, not stored
+    uint32_t q[32];
+    if (r < R) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) q[i] = *reinterpret_cast<const uint32_t*>(ckpt + (r + i) * C + c);
+    }
+    if (r0 + tid < R) {
+#pragma unroll
+        for (int b = 0; b < kReCols / 32; ++b) {
+            const int64_t at = c0 / 32 + b < Cb ? c0 / 32 + b : Cb - 1;
+            sX[tid][b] = ckpt_scales[(r0 + tid) * Cb + at];
+        }
+    }
+    __syncthreads();
+    if (r < R) {
+        uint32_t v[2][32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint2 d = mx_decode4_bf16<FMT>(q[i], mx_scale(sX[32 * rb + i][cq >> 3]));
+            v[0][i] = d.x;
+            v[1][i] = d.y;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            pack_column_pair(v[k], &sC[4 * cq + 2 * k][16 * rb], kTrPitch, &sS[4 * cq + 2 * k][rb], kTrRows / 32);
+    }
+    __syncthreads();
+    store_columns<kReCols>(sC, sS, codes, scales, r0, c0, R, C);
 }
 
 // ---------------------------------------------------------------------------
@@ -450,10 +581,10 @@ hipError_t pack_as(const void* x, const Packed& out, const Chunks& k, hipStream_
     const uint4* xv = static_cast<const uint4*>(x);
     if (k.ragged)
         hipLaunchKernelGGL((pack_kernel<FMT, F32, true>), chunk_grid(k.n), dim3(kBlock), 0, stream,
-                           xv, out.codes, out.scales, k.n, k.P8, k.C8);
+                           xv, out.codes, out.scales, nullptr, nullptr, k.n, k.P8, k.C8);
     else
         hipLaunchKernelGGL((pack_kernel<FMT, F32, false>), chunk_grid(k.n), dim3(kBlock), 0, stream,
-                           xv, out.codes, out.scales, k.n, k.P8, k.C8);
+                           xv, out.codes, out.scales, nullptr, nullptr, k.n, k.P8, k.C8);
     return hipGetLastError();
 }
 
@@ -535,19 +666,53 @@ hipError_t launch_mx4_quantize(const void* x, bool f32, const Packed& out, int64
         const uint4* xv = static_cast<const uint4*>(x);
         if (f32)
             hipLaunchKernelGGL((pack_kernel<kE2M1, true, false>), chunk_grid(k.n), dim3(kBlock), 0,
-                               stream, xv, out.codes, out.scales, k.n, k.P8, k.C8);
+                               stream, xv, out.codes, out.scales, nullptr, nullptr, k.n, k.P8, k.C8);
         else
             hipLaunchKernelGGL((pack_kernel<kE2M1, false, false>), chunk_grid(k.n), dim3(kBlock), 0,
-                               stream, xv, out.codes, out.scales, k.n, k.P8, k.C8);
+                               stream, xv, out.codes, out.scales, nullptr, nullptr, k.n, k.P8, k.C8);
         return hipGetLastError();
     }
     const dim3 grid((unsigned)((R + kTrRows - 1) / kTrRows), (unsigned)((C + kTrCols - 1) / kTrCols));
     if (f32)
-        hipLaunchKernelGGL(pack_transposed_kernel<true>, grid, dim3(kBlock), 0, stream, x,
-                           static_cast<uint8_t*>(out.codes), out.scales, R, C);
+        hipLaunchKernelGGL((pack_transposed_kernel<true, false>), grid, dim3(kBlock), 0, stream, x,
+                           static_cast<uint8_t*>(out.codes), out.scales, nullptr, nullptr, R, C);
     else
-        hipLaunchKernelGGL(pack_transposed_kernel<false>, grid, dim3(kBlock), 0, stream, x,
-                           static_cast<uint8_t*>(out.codes), out.scales, R, C);
+        hipLaunchKernelGGL((pack_transposed_kernel<false, false>), grid, dim3(kBlock), 0, stream, x,
+                           static_cast<uint8_t*>(out.codes), out.scales, nullptr, nullptr, R, C);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_quantize_both(const void* x, bool f32, const Packed& rows, const Packed& cols,
+                                    int64_t R, int64_t C, hipStream_t stream)
+{
+    const int64_t tiles = (R + kTrRows - 1) / kTrRows * ((C + kTrCols - 1) / kTrCols);
+    auto* kernel = f32 ? pack_transposed_kernel<true, true> : pack_transposed_kernel<false, true>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(kBlock), 0, stream, x,
+                       static_cast<uint8_t*>(cols.codes), cols.scales,
+                       static_cast<uint32_t*>(rows.codes), rows.scales, R, C);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_quantize_ckpt(const void* x, bool f32, const Packed& out, const Packed& ckpt,
+                                    int64_t R, int64_t C, int fmt, hipStream_t stream)
+{
+    const Chunks k = chunks_of(R, C);  // C is a multiple of 32
+    auto* kernel = fmt == kE4M3
+                       ? (f32 ? pack_kernel<kE4M3, true, false, true> : pack_kernel<kE4M3, false, false, true>)
+                       : (f32 ? pack_kernel<kInt8, true, false, true> : pack_kernel<kInt8, false, false, true>);
+    hipLaunchKernelGGL(kernel, chunk_grid(k.n), dim3(kBlock), 0, stream, static_cast<const uint4*>(x),
+                       ckpt.codes, ckpt.scales, static_cast<uint32_t*>(out.codes), out.scales, k.n,
+                       k.P8, k.C8);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_requantize(const Packed& ckpt, const Packed& out, int64_t R, int64_t C, int fmt,
+                                 hipStream_t stream)
+{
+    const dim3 grid((unsigned)((R + kTrRows - 1) / kTrRows), (unsigned)((C + kReCols - 1) / kReCols));
+    auto* kernel = fmt == kE4M3 ? repack_transposed_kernel<kE4M3> : repack_transposed_kernel<kInt8>;
+    hipLaunchKernelGGL(kernel, grid, dim3(kBlock), 0, stream, static_cast<const uint8_t*>(ckpt.codes),
+                       ckpt.scales, static_cast<uint8_t*>(out.codes), out.scales, R, C);
     return hipGetLastError();
 }
 

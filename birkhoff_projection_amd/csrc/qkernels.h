@@ -37,6 +37,15 @@ hipError_t launch_stream_mix_bwd_ckpt(const Packed& ckpt, const float* H, const 
                                       hipStream_t stream);
 hipError_t launch_mx4_quantize(const void* x, bool f32, const Packed& out, int64_t R, int64_t C,
                                bool transpose, hipStream_t stream);
+// rows and, transposed, columns of x in one pass
+hipError_t launch_mx4_quantize_both(const void* x, bool f32, const Packed& rows, const Packed& cols,
+                                    int64_t R, int64_t C, hipStream_t stream);
+// rows of x in 4 bits and as an 8-bit checkpoint in one pass
+hipError_t launch_mx4_quantize_ckpt(const void* x, bool f32, const Packed& out, const Packed& ckpt,
+                                    int64_t R, int64_t C, int fmt, hipStream_t stream);
+// the columns of an 8-bit checkpoint [R, C] in 4 bits
+hipError_t launch_mx4_requantize(const Packed& ckpt, const Packed& out, int64_t R, int64_t C, int fmt,
+                                 hipStream_t stream);
 hipError_t launch_mx4_dequantize(const Packed& in, void* x, bool f32, int64_t R, int64_t C,
                                  hipStream_t stream);
 // y [M,N] = a b^T for MXFP4 a [M,K], b [N,K]; f32: y is fp32 instead of bf16.

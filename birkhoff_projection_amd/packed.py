@@ -213,6 +213,33 @@ def mx4_quantize(x: torch.Tensor, *, transpose=False, out=None):
     return codes, scales
 
 
+def mx4_quantize_both(x: torch.Tensor):
+    """mx4_quantize(x) and mx4_quantize(x, transpose=True) in one pass over x
+    [R, C] bf16 or fp32, R and C multiples of 32."""
+    status, codes, scales, t_codes, t_scales = binding().mx4_quantize_both(x)
+    if status:
+        check(status)
+    return (codes, scales), (t_codes, t_scales)
+
+
+def mx4_quantize_ckpt(x: torch.Tensor, *, format="e4m3"):
+    """mx4_quantize(x) and ckpt_pack(x, format=format) in one pass over x
+    [R, C] bf16 or fp32, C a multiple of 32."""
+    status, codes, scales, c_codes, c_scales = binding().mx4_quantize_ckpt(x, _format(format))
+    if status:
+        check(status)
+    return (codes, scales), (c_codes, c_scales)
+
+
+def mx4_requantize(codes: torch.Tensor, scales: torch.Tensor, *, format="e4m3"):
+    """mx4_quantize(ckpt_unpack(codes, scales), transpose=True) in one pass:
+    the quantised transpose of a checkpoint [R, C], R and C multiples of 32."""
+    status, q_codes, q_scales = binding().mx4_requantize(codes, scales, _format(format))
+    if status:
+        check(status)
+    return q_codes, q_scales
+
+
 def mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, *, dtype=torch.bfloat16, out=None):
     """The values of a quantised matrix, [R, C] bf16 or fp32."""
     status, x = binding().mx4_dequantize(codes, scales, _dtype(dtype), out)
@@ -254,9 +281,10 @@ class Mx4Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, format):
         x, w = x.contiguous(), w.contiguous()
-        y = mx4_matmul(x, mx4_quantize(w), out_dtype=x.dtype)
-        codes, scales = ckpt_pack(x, format=format)
-        ctx.format, ctx.dtype = format, x.dtype
+        ctx.format = _format(format)
+        status, y, codes, scales = binding().mx4_linear_fwd(x, w, ctx.format)
+        if status:
+            check(status)
         ctx.save_for_backward(codes, scales, w)
         return y
 
@@ -264,16 +292,14 @@ class Mx4Linear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gy):
         codes, scales, w = ctx.saved_tensors
-        gy = gy.contiguous()
-        gx = gw = None
-        if ctx.needs_input_grad[0]:
-            gx = mx4_matmul(gy, mx4_quantize(w, transpose=True), out_dtype=ctx.dtype)
-        if ctx.needs_input_grad[1] and gy.shape[0] == 0:
-            gw = torch.zeros_like(w)
-        elif ctx.needs_input_grad[1]:
-            x = ckpt_unpack(codes, scales, format=ctx.format, dtype=ctx.dtype)
-            gw = mx4_matmul(mx4_quantize(gy, transpose=True), mx4_quantize(x, transpose=True),
-                            out_dtype=w.dtype)
+        want_x, want_w, _ = ctx.needs_input_grad
+        if gy.shape[0] == 0:
+            return (gy.new_zeros(codes.shape) if want_x else None,
+                    torch.zeros_like(w) if want_w else None, None)
+        status, gx, gw = binding().mx4_linear_bwd(codes, scales, w, gy.contiguous(), ctx.format,
+                                                  want_x, want_w)
+        if status:
+            check(status)
         return gx, gw, None
 
 

@@ -31,7 +31,8 @@
  *                       and the layer step that write them in the forward and
  *                       read them in the backward
  *   mhc_layer_read      the read half of the layer step (maps and u)
- *   mhc_mx4_quantize/dequantize, mhc_mx4_matmul, mhc_mx4_matmul_values,
+ *   mhc_mx4_quantize/_both/_ckpt, mhc_mx4_requantize, mhc_mx4_dequantize,
+ *   mhc_mx4_matmul, mhc_mx4_matmul_values,
  *   mhc_mx4_write_back  microscaled 4-bit quantisation and products for the
  *                       layer function, the last one with the layer's
  *                       write-back in its epilogue
@@ -507,6 +508,24 @@ mhc_status mhc_mx4_quantize(const void* x, int32_t dtype, void* codes, uint8_t* 
                             int64_t C, int32_t transpose, void* stream);
 mhc_status mhc_mx4_dequantize(const void* codes, const uint8_t* scales, void* x, int32_t dtype,
                               int64_t R, int64_t C, void* stream);
+
+/* What a training step of a linear map needs more than one of, in one pass:
+ * mhc_mx4_quantize_both -- mhc_mx4_quantize with transpose = 0 into codes and
+ *   scales and with transpose = 1 into t_codes and t_scales, bit for bit; R and
+ *   C multiples of 32
+ * mhc_mx4_quantize_ckpt -- mhc_mx4_quantize with transpose = 0, and mhc_ckpt_pack
+ *   into ckpt_codes [R, C] and ckpt_scales [R, C/32], bit for bit; C a multiple
+ *   of 32
+ * mhc_mx4_requantize -- the quantised transpose (codes [C, R/2], scales
+ *   [C, R/32]) of the values of a checkpoint [R, C]; R and C multiples of 32
+ * No output may overlap another tensor. */
+mhc_status mhc_mx4_quantize_both(const void* x, int32_t dtype, void* codes, uint8_t* scales,
+                                 void* t_codes, uint8_t* t_scales, int64_t R, int64_t C, void* stream);
+mhc_status mhc_mx4_quantize_ckpt(const void* x, int32_t dtype, void* codes, uint8_t* scales,
+                                 void* ckpt_codes, uint8_t* ckpt_scales, int64_t R, int64_t C,
+                                 int32_t format, void* stream);
+mhc_status mhc_mx4_requantize(const void* ckpt_codes, const uint8_t* ckpt_scales, void* codes,
+                              uint8_t* scales, int64_t R, int64_t C, int32_t format, void* stream);
 
 /* mhc_mx4_matmul -- out[m,n] = sum_k a[m,k] b[n,k] for MXFP4 a [M,K] and
  * b [N,K] (both quantised along the summed axis; a weight matrix of a linear

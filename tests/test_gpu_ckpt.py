@@ -111,6 +111,38 @@ def test_mx4_quantize(gpu_lib, R, C, transpose, dtype):
     assert bool((cb[rows:] == 0x5A).all()) and bool((sb[rows:] == 0x5A).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R,C", [(32, 32), (64, 96), (288, 160), (256, 64), (320, 1088), (2080, 64), (544, 4096)])
+def test_mx4_joint_quantisation(gpu_lib, R, C, dtype):
+    """What one pass writes twice is what two calls write, bit for bit, for
+    values near the formats' limits, infinities and NaN too."""
+    print(f"mx4 joint {R}x{C} {dtype}", flush=True)
+    x = hard_rows(R, C, R + C, dtype)
+    same = lambda a, b: all(torch.equal(p, q) for p, q in zip(a, b))
+    rows, cols = gpu_lib.mx4_quantize_both(x)
+    assert same(rows, gpu_lib.mx4_quantize(x)) and same(cols, gpu_lib.mx4_quantize(x, transpose=True))
+    for fmt in FMTS:
+        q, ck = gpu_lib.mx4_quantize_ckpt(x, format=fmt)
+        assert same(q, rows) and same(ck, gpu_lib.ckpt_pack(x, format=fmt))
+        back = gpu_lib.ckpt_unpack(*ck, format=fmt, dtype=dtype)
+        assert same(gpu_lib.mx4_requantize(*ck, format=fmt), gpu_lib.mx4_quantize(back, transpose=True))
+
+
+def test_mx4_quantize_ckpt_any_rows(gpu_lib):
+    for R in (1, 7, 33):
+        x = rand((R, 96), R)
+        q, ck = gpu_lib.mx4_quantize_ckpt(x, format="int8")
+        for a, b in zip((*q, *ck), (*gpu_lib.mx4_quantize(x), *gpu_lib.ckpt_pack(x, format="int8"))):
+            assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        gpu_lib.mx4_quantize_both(rand((33, 64), 1))
+    with pytest.raises(ValueError):
+        gpu_lib.mx4_quantize_ckpt(rand((32, 40), 1))
+    c, s = gpu_lib.ckpt_pack(rand((32, 64), 1))
+    with pytest.raises(ValueError):
+        gpu_lib.mx4_requantize(c, s[:31])
+
+
 def test_dequantize_reads_any_scale_byte(gpu_lib):
     g = torch.Generator().manual_seed(3)
     codes = torch.randint(0, 256, (256, 32), generator=g, dtype=torch.uint8)

@@ -195,6 +195,18 @@ def test_linear_gradients(gpu_lib, M, N, K, fmt):
         close(gw, Q(f64(gy).T), Q(xh.T), dt, "grad_w")
 
 
+def test_linear_wanted_gradients(gpu_lib):
+    """Each gradient alone is what both together give; no rows give zeros."""
+    x, w, gy = rand((96, 64), 1), rand((160, 64), 2), rand((96, 160), 3)
+    xr, wr = x.clone().requires_grad_(True), w.clone().requires_grad_(True)
+    gx, gw = torch.autograd.grad(gpu_lib.mx4_linear(xr, wr), (xr, wr), gy)
+    assert torch.equal(torch.autograd.grad(gpu_lib.mx4_linear(xr, w), xr, gy)[0], gx)
+    assert torch.equal(torch.autograd.grad(gpu_lib.mx4_linear(x, wr), wr, gy)[0], gw)
+    x0 = x[:0].clone().requires_grad_(True)
+    g0, w0 = torch.autograd.grad(gpu_lib.mx4_linear(x0, wr).sum(), (x0, wr))
+    assert g0.shape == (0, 64) and not bool(w0.any())
+
+
 def test_linear_gradient_by_differences(gpu_lib):
     """With operands that MXFP4 and the checkpoint hold exactly, the map is
     bilinear and a central difference of the loss is its derivative."""

@@ -100,3 +100,31 @@ def test_binding_refusals():
         bp.mx4_linear(torch.zeros(2, 32, 64), torch.zeros(32, 64))
     with pytest.raises(TypeError):
         bp.layer_read(torch.zeros(4, 4, 64), torch.zeros(24, 256))
+
+
+def test_joint_quantisation_errors(L):
+    def both(p=A, dt=0, R=64, C=64):
+        return L.mhc_mx4_quantize_both(p[0], dt, p[1], p[2], p[3], p[4], R, C, None)
+
+    def ckpt(p=A, dt=0, R=64, C=64, fmt=0):
+        return L.mhc_mx4_quantize_ckpt(p[0], dt, p[1], p[2], p[3], p[4], R, C, fmt, None)
+
+    def again(p=A, R=64, C=64, fmt=0):
+        return L.mhc_mx4_requantize(p[0], p[1], p[2], p[3], R, C, fmt, None)
+
+    none = [None] * 5
+    assert both(none, R=0) == 0 and ckpt(none, R=0) == 0 and again(none, R=0) == 0
+
+    def at(k, v):
+        return A[:k] + [v] + A[k + 1:]
+
+    for f, kw, text in ((both, dict(R=40), "R must"), (both, dict(C=40), "C must"), (both, dict(dt=3), "dtype"),
+                        (both, dict(R=-32), "out of range"), (both, dict(p=at(3, None)), "NULL"),
+                        (both, dict(p=at(4, A[2])), "overlaps"), (both, dict(p=at(3, A[0] + 16)), "overlaps"),
+                        (ckpt, dict(C=40), "C must"), (ckpt, dict(fmt=2), "format"), (ckpt, dict(dt=-1), "dtype"),
+                        (ckpt, dict(p=at(1, A[3])), "overlaps"), (ckpt, dict(p=at(4, A[4] + 2)), "aligned"),
+                        (again, dict(R=48), "R must"), (again, dict(C=0), "C must"), (again, dict(fmt=-1), "format"),
+                        (again, dict(C=128 * 65536, R=32), "out of range"), (again, dict(p=at(2, A[0])), "overlaps"),
+                        (again, dict(p=at(1, None)), "NULL")):
+        assert f(**kw) == INVALID, (f.__name__, kw)
+        assert text in _err(L), (f.__name__, kw, _err(L))
