@@ -494,6 +494,7 @@ __global__ __launch_bounds__(kBlock) void stream_mix_ckpt_kernel(
 // Backward.  W = 64: one wave per token at a time (grid-stride); a lane
 // accumulates its chunks' contribution to grad_H in 16 registers, the wave
 // reduces them once per token.  W = 16, for narrow rows: 16 lanes per token.
+// W = 256, for few tokens of wide rows: a workgroup per token.
 template <int FMT, int W>
 __global__ __launch_bounds__(kBlock) void stream_mix_bwd_ckpt_kernel(
     const uint2* __restrict__ codes, const uint8_t* __restrict__ scales,
@@ -546,7 +547,14 @@ __global__ __launch_bounds__(kBlock) void stream_mix_bwd_ckpt_kernel(
                         acc[4 * i + j] = __builtin_fmaf(gf[i][e], xf[e], acc[4 * i + j]);
             }
         }
-        if (W == 64) {
+        if constexpr (W == 256) {
+            __shared__ float sP[4][16];
+            const float sum = wave_sum_halving<16>(acc);
+            if ((lane & 3) == 0) sP[lane >> 6][(lane & 63) >> 2] = sum;
+            __syncthreads();
+            if (lane < 16) gH[16 * t + lane] = (sP[0][lane] + sP[1][lane]) + (sP[2][lane] + sP[3][lane]);
+            return;  // the grid has a workgroup for every token
+        } else if (W == 64) {
             const float sum = wave_sum_halving<16>(acc);
             if ((lane & 3) == 0) gH[16 * t + (lane >> 2)] = sum;
         } else {
@@ -624,17 +632,14 @@ template <int FMT>
 void mix_bwd_ckpt_as(const Packed& ckpt, const float* H, const void* gout, void* gx, float* gH,
                      int64_t T, int64_t C, hipStream_t stream)
 {
-    const bool narrow = C <= 256;
-    const int64_t waves = narrow ? (T + 3) / 4 : T, most = waves < 8192 ? waves : 8192;
-    const dim3 grid((unsigned)((most + 3) / 4));
     const uint2* cv = static_cast<const uint2*>(ckpt.codes);
     const uint4* gv = static_cast<const uint4*>(gout);
-    if (narrow)
-        hipLaunchKernelGGL((stream_mix_bwd_ckpt_kernel<FMT, 16>), grid, dim3(kBlock), 0, stream, cv,
-                           ckpt.scales, H, gv, static_cast<uint4*>(gx), gH, T, C / 8);
-    else
-        hipLaunchKernelGGL((stream_mix_bwd_ckpt_kernel<FMT, 64>), grid, dim3(kBlock), 0, stream, cv,
-                           ckpt.scales, H, gv, static_cast<uint4*>(gx), gH, T, C / 8);
+    const bool narrow = C <= 256, few = T <= 2048 && C > 512;
+    const int64_t waves = narrow ? (T + 3) / 4 : T, most = waves < 8192 ? waves : 8192;
+    auto* kernel = narrow ? stream_mix_bwd_ckpt_kernel<FMT, 16>
+                          : (few ? stream_mix_bwd_ckpt_kernel<FMT, 256> : stream_mix_bwd_ckpt_kernel<FMT, 64>);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(few ? T : (most + 3) / 4)), dim3(kBlock), 0, stream, cv,
+                       ckpt.scales, H, gv, static_cast<uint4*>(gx), gH, T, C / 8);
 }
 
 }  // namespace

@@ -835,11 +835,16 @@ hipError_t layer_mix_as(const LayerPtrs& a, const Packed& x, const Packed& f, in
 
 LayerCkptPlan layer_ckpt_plan(int64_t T, int64_t C)
 {
-    const LayerPlan base = layer_plan(T, C);
     LayerCkptPlan p;
-    p.Tp = base.Tp;
-    p.group_tokens = base.group_tokens;
-    p.groups = base.groups;
+    p.Tp = layer_plan(T, C).Tp;
+    // token groups of the grad_W pass: with C / 64 workgroups to a group, about
+    // 512 in all, but 16 groups at least (the tail is then short) and 64 at
+    // most (their partials are read back); 35928 x 64: 48 us with 16 groups
+    int64_t want = 512 / (C / 64);
+    want = want < 16 ? 16 : (want > 64 ? 64 : want);
+    p.group_tokens = ((p.Tp + want - 1) / want + 127) / 128 * 128;
+    if (p.group_tokens < 128) p.group_tokens = 128;  // no tokens
+    p.groups = (p.Tp + p.group_tokens - 1) / p.group_tokens;
     const int64_t D = 4 * C;
     p.off_s = 0;
     p.off_dl = (p.Tp * 4 + 255) / 256 * 256;

@@ -76,6 +76,7 @@ hipError_t launch_layer_dw_reduce(const float* partial, float* gW, int64_t C, in
 // read_plan().bytes bytes (fp32 partials [splits][T][25]; none for many tokens).
 struct ReadPlan {
     int64_t splits, steps_per, bytes;
+    int tiles;  // of 16 tokens to a workgroup of the partial sums
 };
 ReadPlan read_plan(int64_t T, int64_t C);
 // The maps alone (the same as launch_layer_read's), with the same workspace.

@@ -86,62 +86,84 @@ __global__ __launch_bounds__(kBlock) void read_mix_kernel(const uint4* __restric
     }
 }
 
-// Partial logits: 4 waves take the 32-wide steps of the workgroup's piece of
-// the width in turn.  MFMA 16x16x32: A = x rows (token l % 16, k 8 (l / 16)),
-// B = W rows (map l % 16), D lane l, v: token 4 (l / 16) + v, map l % 16.
+// Partial logits of NT tiles of 16 tokens: 4 waves take the 32-wide steps of
+// the workgroup's piece of the width in turn.  MFMA 16x16x32: A = x rows (token
+// l % 16, k 8 (l / 16)), B = W rows (map l % 16), D lane l, v: token
+// 4 (l / 16) + v, map l % 16.  Each step of W comes from the caches anew, half
+// again as many bytes as x of one tile: with enough tokens NT is 4.
 constexpr int kPartTok = 16;
 
+template <int NT>
 __global__ __launch_bounds__(kBlock) void read_part_kernel(const uint16_t* __restrict__ x,
                                                            const uint16_t* __restrict__ W,
                                                            float* __restrict__ partial, int64_t T,
                                                            int64_t D, int64_t steps_per)
 {
-    __shared__ float sR[4][kPartTok][32];
-    __shared__ float sQ[4][kPartTok];
+    constexpr int kTok = kPartTok * NT;
+    __shared__ float sR[4][kTok][kMaps + 1];
+    __shared__ float sQ[4][kTok];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int row = lane & 15, kq = lane >> 4;
-    const int64_t t0 = (int64_t)blockIdx.x * kPartTok;
-    int64_t t = t0 + row;
-    t = t < T ? t : T - 1;
-    const uint16_t* xp = x + t * D + 8 * kq;
+    const int64_t t0 = (int64_t)blockIdx.x * kTok;
+    const uint16_t* xp[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int64_t t = t0 + kPartTok * j + row;
+        xp[j] = x + (t < T ? t : T - 1) * D + 8 * kq;
+    }
     const uint16_t* w0 = W + row * D + 8 * kq;
     const uint16_t* w1 = W + (16 + (row & 7)) * D + 8 * kq;  // maps 16..23, twice
     const int64_t s0 = (int64_t)blockIdx.y * steps_per;
     int64_t s1 = s0 + steps_per;
     s1 = s1 < D / 32 ? s1 : D / 32;
-    floatx4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = acc0;
-    float ssq = 0.f;
-    for (int64_t s = s0 + w; s < s1; s += 16) {  // 4 steps' loads at once
-        uint4 a[4], b0[4], b1[4];
+    floatx4 acc0[NT], acc1[NT];
+    float ssq[NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < NT; ++j) {
+        acc0[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+        acc1[j] = acc0[j];
+        ssq[j] = 0.f;
+    }
+    constexpr int kAhead = 4;  // steps' loads at once
+    for (int64_t s = s0 + w; s < s1; s += 4 * kAhead) {
+        uint4 a[kAhead][NT], b0[kAhead], b1[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
             const int64_t at = s + 4 * i < s1 ? s + 4 * i : s;
-            a[i] = *reinterpret_cast<const uint4*>(xp + 32 * at);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) a[i][j] = *reinterpret_cast<const uint4*>(xp[j] + 32 * at);
             b0[i] = *reinterpret_cast<const uint4*>(w0 + 32 * at);
             b1[i] = *reinterpret_cast<const uint4*>(w1 + 32 * at);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kAhead; ++i) {
             if (s + 4 * i >= s1) break;
-            acc0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, a[i]), __builtin_bit_cast(bf16x8, b0[i]), acc0, 0, 0, 0);
-            acc1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, a[i]), __builtin_bit_cast(bf16x8, b1[i]), acc1, 0, 0, 0);
-            float f[8];
-            mx_unpack8(a[i], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ssq = __builtin_fmaf(f[e], f[e], ssq);
+            for (int j = 0; j < NT; ++j) {
+                acc0[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, a[i][j]), __builtin_bit_cast(bf16x8, b0[i]), acc0[j], 0, 0, 0);
+                acc1[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, a[i][j]), __builtin_bit_cast(bf16x8, b1[i]), acc1[j], 0, 0, 0);
+                float f[8];
+                mx_unpack8(a[i][j], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ssq[j] = __builtin_fmaf(f[e], f[e], ssq[j]);
+            }
         }
     }
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        sR[w][4 * kq + v][row] = acc0[v];
-        if (row < 8) sR[w][4 * kq + v][16 + row] = acc1[v];
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            float* d = sR[w][kPartTok * j + 4 * kq + v];
+            d[row] = acc0[j][v];
+            if (row < 8) d[16 + row] = acc1[j][v];
+        }
+        const float q = sum_bit5(sum_bit4(ssq[j]));
+        if (kq == 0) sQ[w][kPartTok * j + row] = q;
     }
-    ssq = sum_bit5(sum_bit4(ssq));
-    if (kq == 0) sQ[w][row] = ssq;
     __syncthreads();
-    for (int p = threadIdx.x; p < kPartTok * kVals; p += kBlock) {
+    for (int p = threadIdx.x; p < kTok * kVals; p += kBlock) {
         const int tl = p / kVals, m = p % kVals;
         if (t0 + tl >= T) break;
         const float v = m < kMaps ? (sR[0][tl][m] + sR[1][tl][m]) + (sR[2][tl][m] + sR[3][tl][m])
@@ -214,16 +236,21 @@ __global__ __launch_bounds__(kBlock) void read_finish_kernel(
 
 }  // namespace
 
-// Up to kReadFewTokens tokens take the split kernels, with about 512
-// workgroups in all and at least 16 steps of 32 (4 per wave) each.
-constexpr int64_t kReadFewTokens = 2048;
+// Up to kReadFewTokens tokens take the split kernels, and up to
+// kReadFewWideTokens of rows wide enough: about 512 workgroups in all (1024
+// are no faster) of at least 16 steps of 32 (4 per wave) each.  Maps and u, us,
+// against the maps pass over whole rows, whose workgroups then are few: 4096 x
+// 7168 87 / 155, 8192 x 7168 201 / 210, 8192 x 2048 58 / 65; but 8192 x 1024
+// 43 / 36 and 4096 x 512 24 / 18 (a workgroup per token for the second half).
+constexpr int64_t kReadFewTokens = 2048, kReadFewWideTokens = 8192, kReadWide = 2048;
 
 ReadPlan read_plan(int64_t T, int64_t C)
 {
-    ReadPlan p{0, 0, 0};
-    if (T <= 0 || T > kReadFewTokens) return p;
-    const int64_t steps = 4 * C / 32, tiles = (T + kPartTok - 1) / kPartTok;
-    int64_t want = (512 + tiles - 1) / tiles;
+    ReadPlan p{0, 0, 0, 1};
+    if (T <= 0 || T > (C >= kReadWide ? kReadFewWideTokens : kReadFewTokens)) return p;
+    p.tiles = T >= 512 ? 4 : 1;
+    const int64_t steps = 4 * C / 32, groups = (T + kPartTok * p.tiles - 1) / (kPartTok * p.tiles);
+    int64_t want = (512 + groups - 1) / groups;
     if (want > steps / 16) want = steps / 16;
     if (want < 1) want = 1;
     p.steps_per = (steps + want - 1) / want;
@@ -237,10 +264,10 @@ static hipError_t launch_split(const LayerPtrs& a, const ReadPlan& p, const UOut
                                int64_t C, float eps, const SolverOpts& o, hipStream_t stream)
 {
     float* partial = static_cast<float*>(a.workspace);
-    hipLaunchKernelGGL(read_part_kernel,
-                       dim3((unsigned)((T + kPartTok - 1) / kPartTok), (unsigned)p.splits),
-                       dim3(kBlock), 0, stream, (const uint16_t*)a.x, (const uint16_t*)a.W, partial,
-                       T, 4 * C, p.steps_per);
+    const int64_t tok = kPartTok * p.tiles;
+    auto* part = p.tiles == 4 ? read_part_kernel<4> : read_part_kernel<1>;
+    hipLaunchKernelGGL(part, dim3((unsigned)((T + tok - 1) / tok), (unsigned)p.splits), dim3(kBlock), 0,
+                       stream, (const uint16_t*)a.x, (const uint16_t*)a.W, partial, T, 4 * C, p.steps_per);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (o.solver == 0)

@@ -134,9 +134,9 @@ def layer_fwd_ckpt(x, W, f, *, format="e4m3", eps=1e-6, solver="newton", max_ite
                    warm_sweeps=None, out=None, ckpt=None):
     """``layer_fwd`` that also writes the checkpoints of x and f.  Returns
     (forward dict, dict(x=(codes, scales), f=(codes, scales))).  The maps are
-    layer_read's bit for bit, and above 2048 tokens all of the forward is
-    layer_fwd's.  Only the checkpoints and the forward's rms, logits and maps
-    are needed by layer_bwd_ckpt.  ``out`` and ``ckpt`` may be previous
+    layer_read's bit for bit; with more than 2048 tokens (8192 where C is
+    2048 or more) all of the forward is layer_fwd's.  Only the checkpoints and
+    the forward's rms, logits and maps are needed by layer_bwd_ckpt.  ``out`` and ``ckpt`` may be previous
     results."""
     out, ckpt = out or {}, ckpt or {}
     status, maps, (u, x_out), k = binding().layer_fwd_ckpt(

@@ -470,11 +470,10 @@ typedef struct {
 /* mhc_layer_fwd_ckpt -- mhc_layer_fwd that also writes the checkpoints of x
  * and f, in the pass that reads both.  rms, logits and the maps are
  * mhc_layer_read's, with its workspace in a->workspace (a->workspace_bytes at
- * least mhc_layer_read_workspace_bytes(), 0 above 2048 tokens): above 2048
- * tokens every output is mhc_layer_fwd's bit for bit, below the sums behind
- * the maps are added in another order.  No output may overlap another tensor;
- * the workspace must not be in use by another call that overlaps on the
- * device. */
+ * least mhc_layer_read_workspace_bytes()): where that is 0 every output is
+ * mhc_layer_fwd's bit for bit, elsewhere the sums behind the maps are added in
+ * another order.  No output may overlap another tensor; the workspace must not
+ * be in use by another call that overlaps on the device. */
 mhc_status mhc_layer_fwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* ckpt, void* stream);
 
 /* mhc_layer_bwd_ckpt -- mhc_layer_bwd from the checkpoints: xhat and fhat in
@@ -564,12 +563,14 @@ mhc_status mhc_mx4_write_back(const void* a_codes, const uint8_t* a_scales, cons
  * yet: rms, logits, H_pre, H_post, H_res and u from x and W, as mhc_layer_fwd
  * (f and x_out are ignored).  u goes to a->u (bf16) and, if u_codes and
  * u_scales are given, also or instead (a->u NULL) to MXFP4 ([T, C/2] and
- * [T, C/32]): mhc_mx4_quantize of the bf16 u.  Up to 2048 tokens the width is
- * split over the GPU, with fp32 partial sums in a->workspace (16-byte aligned,
- * at least mhc_layer_read_workspace_bytes() bytes; 0 means none is needed), and
- * the sums differ from mhc_layer_fwd's in their order; above that the maps are
- * mhc_layer_fwd's, bit for bit.  No output may overlap another tensor; the
- * workspace must not be in use by another call that overlaps on the device. */
+ * [T, C/32]): mhc_mx4_quantize of the bf16 u.  Up to 2048 tokens, and up to
+ * 8192 where C is 2048 or more, the width is split over the GPU, with fp32
+ * partial sums in a->workspace (16-byte aligned, at least
+ * mhc_layer_read_workspace_bytes() bytes), and the sums differ from
+ * mhc_layer_fwd's in their order; with more tokens no workspace is needed (0
+ * bytes) and the maps are mhc_layer_fwd's, bit for bit.  No output may overlap
+ * another tensor; the workspace must not be in use by another call that
+ * overlaps on the device. */
 int64_t mhc_layer_read_workspace_bytes(int64_t T, int32_t n, int64_t C);
 mhc_status mhc_layer_read(const mhc_layer_args* a, void* u_codes, uint8_t* u_scales, void* stream);
 

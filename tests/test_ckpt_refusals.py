@@ -105,6 +105,7 @@ def test_layer_errors(L):
         assert f(ctypes.byref(a), ctypes.byref(k), None) == 0
     assert L.mhc_layer_read_workspace_bytes(0, 4, 64) == 0  # no tokens
     assert L.mhc_layer_read_workspace_bytes(2049, 4, 64) == 0
+    assert L.mhc_layer_ckpt_workspace_bytes(0, 4, 64) >= 0
     a, k = _layer()
     a.workspace_bytes = L.mhc_layer_read_workspace_bytes(16, 4, 64) - 1
     assert L.mhc_layer_fwd_ckpt(ctypes.byref(a), ctypes.byref(k), None) == INVALID
