@@ -12,7 +12,7 @@ from .ops import (BirkhoffProjection, birkhoff_bwd, birkhoff_bwd_n, birkhoff_bwd
                   birkhoff_project,
                   layer_bwd, layer_bwd_noalloc, layer_fwd, layer_workspace, make_opts,
                   stream_mix, stream_mix_bwd)
-from .packed import (Mx4Linear, ProjectedMix, ckpt_pack, ckpt_unpack, layer_bwd_ckpt,
+from .packed import (ProjectedMix, ckpt_pack, ckpt_unpack, layer_bwd_ckpt,
                      layer_ckpt_workspace, layer_fwd_ckpt, layer_read, mx4_dequantize, mx4_linear,
                      mx4_matmul, mx4_quantize, mx4_quantize_both, mx4_quantize_ckpt, mx4_requantize,
                      mx4_write_back, projected_mix, stream_mix_bwd_ckpt,
@@ -23,7 +23,7 @@ __all__ = ["LIB_PATH", "MHCError", "lib", "BirkhoffProjection", "birkhoff_bwd",
            "birkhoff_fwd", "birkhoff_pipeline_step", "birkhoff_project", "layer_bwd", "layer_bwd_noalloc", "layer_fwd",
            "layer_workspace",
            "make_opts", "stream_mix", "stream_mix_bwd",
-           "Mx4Linear", "ProjectedMix", "ckpt_pack", "ckpt_unpack", "layer_bwd_ckpt",
+           "ProjectedMix", "ckpt_pack", "ckpt_unpack", "layer_bwd_ckpt",
            "layer_ckpt_workspace", "layer_fwd_ckpt", "layer_read", "mx4_dequantize", "mx4_linear",
            "mx4_matmul", "mx4_quantize", "mx4_quantize_both", "mx4_quantize_ckpt", "mx4_requantize",
            "mx4_write_back", "projected_mix", "stream_mix_bwd_ckpt",

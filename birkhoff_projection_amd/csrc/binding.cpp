@@ -11,6 +11,8 @@
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <tuple>
@@ -503,47 +505,84 @@ std::tuple<int, Tensor> mx4_write_back(const Tensor& ac, const Tensor& as, const
     return {st, std::move(y)};
 }
 
-// A linear map's forward: y = q(x) q(w)^T, and x as a checkpoint.  Returns y
-// and the checkpoint's codes and scales.
-std::tuple<int, Tensor, Tensor, Tensor> mx4_linear_fwd(const Tensor& x, const Tensor& w, int32_t format)
+void checked(int st)
 {
-    auto [sx, xc, xs, codes, scales] = mx4_quantize_ckpt(x, format);
-    auto [sw, wc, ws] = mx4_quantize(w, false, Opt(), Opt());
-    int st = sx != MHC_OK ? sx : sw;
-    Tensor y;
-    if (st == MHC_OK) std::tie(st, y) = mx4_matmul(xc, xs, wc, ws, values(x, "x"), Opt());
-    return {st, std::move(y), std::move(codes), std::move(scales)};
+    TORCH_CHECK(st == MHC_OK, "mhc: ", mhc_last_error());
 }
 
-// Its backward: grad_x = q(gy) q(w^T)^T and grad_w = q(gy^T) q(xhat^T)^T, each
-// if wanted; M > 0.
-std::tuple<int, Opt, Opt> mx4_linear_bwd(const Tensor& codes, const Tensor& scales, const Tensor& w,
-                                         const Tensor& gy, int32_t format, bool want_x, bool want_w)
+// y = q(x) q(w)^T; grad_x = q(gy) q(w^T)^T and grad_w = q(gy^T) q(xhat^T)^T, with
+// x kept as the checkpoint xhat.  A node of its own, so that the backward runs
+// on autograd's thread without Python.
+struct Mx4Linear : torch::autograd::Function<Mx4Linear> {
+    static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& x0, const Tensor& w0,
+                          int64_t format)
+    {
+        const Tensor x = x0.contiguous(), w = w0.contiguous();
+        auto [sx, xc, xs, codes, scales] = mx4_quantize_ckpt(x, (int32_t)format);
+        checked(sx);
+        auto [sw, wc, ws] = mx4_quantize(w, false, Opt(), Opt());
+        checked(sw);
+        auto [sy, y] = mx4_matmul(xc, xs, wc, ws, values(x, "x"), Opt());
+        checked(sy);
+        ctx->save_for_backward({codes, scales, w});
+        ctx->saved_data["format"] = format;
+        return y;
+    }
+
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                   torch::autograd::variable_list grads)
+    {
+        const auto saved = ctx->get_saved_variables();
+        const Tensor &codes = saved[0], &scales = saved[1], &w = saved[2];
+        const int32_t format = (int32_t)ctx->saved_data["format"].toInt();
+        const bool want_x = ctx->needs_input_grad(0), want_w = ctx->needs_input_grad(1);
+        const bool twice = at::GradMode::is_enabled();
+        const at::AutoGradMode no_grad(false);
+        if (!grads[0].defined()) return {Tensor(), Tensor(), Tensor()};
+        const Tensor gy = grads[0].contiguous();
+        Tensor gx, gw;
+        if (gy.size(0) == 0) {
+            if (want_x) gx = at::zeros(codes.sizes(), gy.options());
+            if (want_w) gw = at::zeros_like(w);
+        } else {
+            Pair r, t;
+            int st = MHC_OK;
+            if (want_x && want_w)
+                std::tie(st, r.codes, r.scales, t.codes, t.scales) = mx4_quantize_both(gy);
+            else if (want_x)
+                std::tie(st, r.codes, r.scales) = mx4_quantize(gy, false, Opt(), Opt());
+            else if (want_w)
+                std::tie(st, t.codes, t.scales) = mx4_quantize(gy, true, Opt(), Opt());
+            checked(st);
+            if (want_x) {
+                auto [sw, wc, ws] = mx4_quantize(w, true, Opt(), Opt());
+                checked(sw);
+                std::tie(st, gx) = mx4_matmul(r.codes, r.scales, wc, ws, values(gy, "grad"), Opt());
+                checked(st);
+            }
+            if (want_w) {
+                auto [sx, xc, xs] = mx4_requantize(codes, scales, format);
+                checked(sx);
+                std::tie(st, gw) = mx4_matmul(t.codes, t.scales, xc, xs, values(w, "w"), Opt());
+                checked(st);
+            }
+        }
+        if (!twice) return {gx, gw, Tensor()};
+        // create_graph: a second derivative raises instead of being zero
+        torch::autograd::variable_list out{gx, gw};
+        for (Tensor& g : out)
+            if (g.defined()) {
+                const auto error = std::make_shared<torch::autograd::DelayedError>(
+                    "mx4_linear is differentiable once", 1);
+                g = (*error)({g.detach().set_requires_grad(true)})[0];
+            }
+        return {out[0], out[1], Tensor()};
+    }
+};
+
+Tensor mx4_linear(const Tensor& x, const Tensor& w, int32_t format)
 {
-    Opt gx, gw;
-    Pair r, t;
-    int st = MHC_OK;
-    if (want_x && want_w)
-        std::tie(st, r.codes, r.scales, t.codes, t.scales) = mx4_quantize_both(gy);
-    else if (want_x)
-        std::tie(st, r.codes, r.scales) = mx4_quantize(gy, false, Opt(), Opt());
-    else if (want_w)
-        std::tie(st, t.codes, t.scales) = mx4_quantize(gy, true, Opt(), Opt());
-    if (st == MHC_OK && want_x) {
-        Tensor y;
-        auto [sw, wc, ws] = mx4_quantize(w, true, Opt(), Opt());
-        st = sw;
-        if (st == MHC_OK) std::tie(st, y) = mx4_matmul(r.codes, r.scales, wc, ws, values(gy, "grad"), Opt());
-        gx = std::move(y);
-    }
-    if (st == MHC_OK && want_w) {
-        Tensor y;
-        auto [sx, xc, xs] = mx4_requantize(codes, scales, format);
-        st = sx;
-        if (st == MHC_OK) std::tie(st, y) = mx4_matmul(t.codes, t.scales, xc, xs, values(w, "w"), Opt());
-        gw = std::move(y);
-    }
-    return {st, std::move(gx), std::move(gw)};
+    return Mx4Linear::apply(x, w, (int64_t)format);
 }
 
 }  // namespace
@@ -565,6 +604,5 @@ PYBIND11_MODULE(_binding, m)
     m.def("mx4_matmul", &mx4_matmul);
     m.def("mx4_matmul_values", &mx4_matmul_values);
     m.def("mx4_write_back", &mx4_write_back);
-    m.def("mx4_linear_fwd", &mx4_linear_fwd);
-    m.def("mx4_linear_bwd", &mx4_linear_bwd);
+    m.def("mx4_linear", &mx4_linear);
 }

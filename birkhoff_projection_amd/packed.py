@@ -275,43 +275,15 @@ def mx4_write_back(a, b, x, H_post, H_res, *, out=None, f_out=None):
     return y
 
 
-class Mx4Linear(torch.autograd.Function):
-    """y = x w^T with every product on MXFP4 operands (see mx4_linear)."""
-
-    @staticmethod
-    def forward(ctx, x, w, format):
-        x, w = x.contiguous(), w.contiguous()
-        ctx.format = _format(format)
-        status, y, codes, scales = binding().mx4_linear_fwd(x, w, ctx.format)
-        if status:
-            check(status)
-        ctx.save_for_backward(codes, scales, w)
-        return y
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, gy):
-        codes, scales, w = ctx.saved_tensors
-        want_x, want_w, _ = ctx.needs_input_grad
-        if gy.shape[0] == 0:
-            return (gy.new_zeros(codes.shape) if want_x else None,
-                    torch.zeros_like(w) if want_w else None, None)
-        status, gx, gw = binding().mx4_linear_bwd(codes, scales, w, gy.contiguous(), ctx.format,
-                                                  want_x, want_w)
-        if status:
-            check(status)
-        return gx, gw, None
-
-
 def mx4_linear(x, w, *, format="e4m3"):
     """Differentiable y = x w^T [M, N] for x [M, K], w [N, K] bf16 or fp32 (M,
     N and K multiples of 32).  Each of the three products takes both operands
     in MXFP4, quantised along the axis it sums over: y = q(x) q(w)^T,
     grad_x = q(gy) q(w^T)^T, grad_w = q(gy^T) q(xhat^T)^T.  x is kept for the
-    backward as an 8-bit checkpoint (xhat), w as it is."""
+    backward as an 8-bit checkpoint (xhat), w as it is.  Differentiable once."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be [M, K] and [N, K]")
     if any(s % BLOCK for s in (*x.shape, *w.shape)):
         raise ValueError(f"M, N and K must be multiples of {BLOCK}, got x {tuple(x.shape)} and "
                          f"w {tuple(w.shape)}")
-    return Mx4Linear.apply(x, w, format)
+    return binding().mx4_linear(x, w, _format(format))

@@ -207,6 +207,36 @@ def test_linear_wanted_gradients(gpu_lib):
     assert g0.shape == (0, 64) and not bool(w0.any())
 
 
+def test_linear_strides_and_refusals(gpu_lib):
+    """Strided operands and gradients count by value; a second derivative, a
+    weight changed in place and wrong tensors raise."""
+    x, w, gy = rand((96, 64), 1), rand((160, 64), 2), rand((96, 160), 3)
+    ref = [t.clone().requires_grad_(True) for t in (x, w)]
+    y = gpu_lib.mx4_linear(*ref)
+    want = torch.autograd.grad(y, ref, gy)
+    odd = [t.t().contiguous().t().requires_grad_(True) for t in (x, w)]
+    got = torch.autograd.grad(gpu_lib.mx4_linear(*odd), odd, gy.t().contiguous().t())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y = gpu_lib.mx4_linear(*ref)
+    first = torch.autograd.grad(y, ref, gy, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(first, want))
+    with pytest.raises(RuntimeError, match="once"):
+        (first[0].float().sum() + first[1].float().sum()).backward()
+    y = gpu_lib.mx4_linear(*ref)
+    with torch.no_grad():
+        ref[1].mul_(2.0)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+    for a, b in ((x.cpu(), w), (x, w.cpu()), (x.half(), w), (x, w.double())):
+        with pytest.raises((TypeError, ValueError)):
+            gpu_lib.mx4_linear(a, b)
+    with pytest.raises(ValueError):
+        gpu_lib.mx4_linear(x, rand((160, 96), 2))
+    with pytest.raises(ValueError):
+        gpu_lib.mx4_linear(x[:95], w)
+    assert not gpu_lib.mx4_linear(x, w).requires_grad
+
+
 def test_linear_gradient_by_differences(gpu_lib):
     """With operands that MXFP4 and the checkpoint hold exactly, the map is
     bilinear and a central difference of the loss is its derivative."""
