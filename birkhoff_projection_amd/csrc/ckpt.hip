@@ -304,28 +304,43 @@ __global__ __launch_bounds__(kBlock) void pack_transposed_kernel(
     __syncthreads();
     store_columns<kTrCols>(sC, sS, codes, scales, r0, c0, R, C);
     if constexpr (ROWS) {
-        // 8 columns per lane; C is a multiple of 32 here, so a quad is whole
+        // 16 columns per lane, a block per pair of lanes; C is a multiple of 32
 #pragma unroll
-        for (int j = 0; j < kTrRows * 8 / kBlock; ++j) {
-            const int p = tid + kBlock * j, row = p >> 3, c8 = p & 7;
-            const int64_t rr = r0 + row, cc = c0 + 8 * c8;
-            const uint4* q = reinterpret_cast<const uint4*>(&sV[row ^ ((row >> 5) & 1)][kRowWords / 8 * c8]);
-            uint32_t amax, s, o;
+        for (int j = 0; j < kTrRows * 4 / kBlock; ++j) {
+            const int p = tid + kBlock * j, row = p >> 2, c16 = p & 3;
+            const int64_t rr = r0 + row, cc = c0 + 16 * c16;
+            const uint4* q = reinterpret_cast<const uint4*>(&sV[row ^ ((row >> 5) & 1)][kRowWords / 4 * c16]);
+            float f[F32 ? 16 : 1];
+            uint4 v[2];
+            uint32_t amax;
             if constexpr (F32) {
-                const float4 a = __builtin_bit_cast(float4, q[0]), b = __builtin_bit_cast(float4, q[1]);
-                float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                amax = mx_quad_max(mx_amax8(f));
-                s = mx_scale_byte<kE2M1>(amax);
-                o = mx_encode8_e2m1(f, amax, s);
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const float4 a = __builtin_bit_cast(float4, q[h]);
+                    f[4 * h] = a.x;
+                    f[4 * h + 1] = a.y;
+                    f[4 * h + 2] = a.z;
+                    f[4 * h + 3] = a.w;
+                }
+                const uint32_t m0 = mx_amax8(f), m1 = mx_amax8(f + 8);
+                amax = m0 > m1 ? m0 : m1;
             } else {
-                const uint4 v = q[0];
-                amax = mx_quad_max(mx_amax8(v));
-                s = mx_scale_byte<kE2M1>(amax);
-                o = mx_encode8_e2m1(v, amax, s);
+                v[0] = q[0];
+                v[1] = q[1];
+                const uint32_t m0 = mx_amax8(v[0]), m1 = mx_amax8(v[1]);
+                amax = m0 > m1 ? m0 : m1;
             }
+            const uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0xB1, 0xF, 0xF, true);
+            amax = other > amax ? other : amax;
+            const uint32_t s = mx_scale_byte<kE2M1>(amax);
+            uint2 o;
+            if constexpr (F32)
+                o = make_uint2(mx_encode8_e2m1(f, amax, s), mx_encode8_e2m1(f + 8, amax, s));
+            else
+                o = make_uint2(mx_encode8_e2m1(v[0], amax, s), mx_encode8_e2m1(v[1], amax, s));
             if (rr < R && cc < C) {
-                row_codes[(rr * C + cc) / 8] = o;
-                if ((c8 & 3) == 0) row_scales[(rr * C + cc) / 32] = (uint8_t)s;
+                *reinterpret_cast<uint2*>(&row_codes[(rr * C + cc) / 8]) = o;
+                if ((c16 & 1) == 0) row_scales[(rr * C + cc) / 32] = (uint8_t)s;
             }
         }
     }
