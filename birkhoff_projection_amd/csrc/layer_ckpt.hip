@@ -655,6 +655,8 @@ struct DwLoads {
     uint32_t s[8];
 };
 
+// tc is wave-uniform: every load is a scalar base plus a 32-bit lane offset (at
+// most 31 rows of 2^26 bytes), which keeps 64-bit sums off the vector unit.
 MHC_DEV void dw_issue(DwLoads& d, const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
                       const __bf16* __restrict__ dlT, int64_t tc, int64_t T, int64_t Tp, int64_t D,
                       int64_t k0, int lane)
@@ -662,20 +664,25 @@ MHC_DEV void dw_issue(DwLoads& d, const uint8_t* __restrict__ xc, const uint8_t*
     const int row = lane & 15, kq = lane >> 4;
     // chunks past the group read a clamped chunk and are not accumulated
     const int64_t ta = tc + 32 < Tp ? tc : Tp - 32;
+    const __bf16* ab = dlT + dl_at(ta, 0, 0);
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-        const int m = 16 * mt + row < kMaps ? 16 * mt + row : kMaps - 1;
+        const uint32_t m = 16 * mt + row < kMaps ? 16 * mt + row : kMaps - 1;
 #pragma unroll
         for (int p = 0; p < kDlParts; ++p)
-            d.a[p][mt] = *reinterpret_cast<const uint4*>(dlT + dl_at(ta, p, m) + 8 * kq);
+            d.a[p][mt] = *reinterpret_cast<const uint4*>(ab + p * (kMaps * 32) + (32u * m + 8u * kq));
     }
-    const int64_t k = k0 + 8 * row;
+    const int64_t tb = tc < T ? tc : T - 1;
+    const uint8_t* cb = xc + tb * D + k0;
+    const uint8_t* sb = xs + (tb * D + k0) / 32;
+    const int last = (int)(T - tb < 32 ? T - tb : 32) - 1 - 8 * kq;  // e of the lane's last token, below 0 if none
+    const uint32_t cD = (uint32_t)D, sD = cD / 32, r0 = 8u * kq;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        int64_t t = tc + 8 * kq + e;
-        t = t < T ? t : T - 1;
-        d.x[e] = *reinterpret_cast<const uint2*>(xc + t * D + k);
-        d.s[e] = xs[t * (D / 32) + (k >> 5)];
+        const uint32_t co = e <= last ? r0 * cD + e * cD : (r0 + last) * cD;
+        const uint32_t so = e <= last ? r0 * sD + e * sD : (r0 + last) * sD;
+        d.x[e] = *reinterpret_cast<const uint2*>(cb + (co + 8u * row));
+        d.s[e] = sb[so + row / 4u];
     }
 }
 
@@ -688,6 +695,7 @@ MHC_DEV void dw_consume(const DwLoads& d, floatx4 (&acc)[2][kDwNt], bool live)
         uint2 v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = mx_decode4_bf16<FMT>(h ? d.x[e].y : d.x[e].x, mx_scale(d.s[e]));
+        bf16x8 bb[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const uint32_t sel = q & 1 ? 0x07060302u : 0x05040100u;
@@ -695,16 +703,19 @@ MHC_DEV void dw_consume(const DwLoads& d, floatx4 (&acc)[2][kDwNt], bool live)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 b[i] = q < 2 ? mx_perm(v[2 * i + 1].x, v[2 * i].x, sel) : mx_perm(v[2 * i + 1].y, v[2 * i].y, sel);
-            const bf16x8 bb = as_bf16x8(make_uint4(b[0], b[1], b[2], b[3]));
-            // A rows 24..31 repeat map 23 (clamped load); they only feed D
-            // rows 24..31, which are never stored.  Smallest parts first.
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-                for (int p = kDlParts - 1; p >= 0; --p)
-                    acc[mt][4 * h + q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        as_bf16x8(d.a[p][mt]), bb, acc[mt][4 * h + q], 0, 0, 0);
+            bb[q] = as_bf16x8(make_uint4(b[0], b[1], b[2], b[3]));
         }
+        // A rows 24..31 repeat map 23 (clamped load); they only feed D rows
+        // 24..31, which are never stored.  Smallest parts first; the parts of
+        // one tile are 8 products apart, so none waits for the one before.
+#pragma unroll
+        for (int p = kDlParts - 1; p >= 0; --p)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+                    acc[mt][4 * h + q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        as_bf16x8(d.a[p][mt]), bb[q], acc[mt][4 * h + q], 0, 0, 0);
     }
 }
 
@@ -714,7 +725,7 @@ __global__ __launch_bounds__(kBlock) void layer_dw_ckpt_kernel(
     float* __restrict__ partial, int64_t T, int64_t Tp, int64_t C, int64_t group_tokens)
 {
     __shared__ __attribute__((aligned(16))) float sR[4][kMaps][kDwK + 4];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kq = lane >> 4;
     const int64_t D = 4 * C;
     const int half = w & 1, phase = w >> 1;
