@@ -10,6 +10,7 @@
 // before anything is enqueued.
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
@@ -505,6 +506,30 @@ std::tuple<int, Tensor> mx4_write_back(const Tensor& ac, const Tensor& as, const
     return {st, std::move(y)};
 }
 
+// Inside a backward that is being captured: does a gradient go on to a node
+// whose stream is the default one, that is, to a graph begun eagerly?  The
+// engine would make that stream wait for the capture, which HIP refuses, and
+// the process ends on it; so the node before it raises instead.
+bool leaves_capture()
+{
+    const auto node = torch::autograd::get_current_node();
+    if (node == nullptr || c10::hip::currentStreamCaptureStatusMayInitCtx() != c10::hip::CaptureStatus::Active)
+        return false;
+    for (const auto& edge : node->next_edges()) {
+        if (!edge.is_valid()) continue;
+        const auto stream = edge.function->stream();
+        if (stream.has_value() && stream->id() == 0) return true;
+    }
+    return false;
+}
+
+void stays_in_capture()
+{
+    TORCH_CHECK(!leaves_capture(),
+                "a captured backward reaches an eager graph on the default stream: drop what holds that graph, or "
+                "capture with leaves of its own");
+}
+
 void checked(int st)
 {
     TORCH_CHECK(st == MHC_OK, "mhc: ", mhc_last_error());
@@ -538,6 +563,7 @@ struct Mx4Linear : torch::autograd::Function<Mx4Linear> {
         const bool want_x = ctx->needs_input_grad(0), want_w = ctx->needs_input_grad(1);
         const bool twice = at::GradMode::is_enabled();
         const at::AutoGradMode no_grad(false);
+        stays_in_capture();
         if (!grads[0].defined()) return {Tensor(), Tensor(), Tensor()};
         const Tensor gy = grads[0].contiguous();
         Tensor gx, gw;
@@ -605,4 +631,5 @@ PYBIND11_MODULE(_binding, m)
     m.def("mx4_matmul_values", &mx4_matmul_values);
     m.def("mx4_write_back", &mx4_write_back);
     m.def("mx4_linear", &mx4_linear);
+    m.def("stays_in_capture", &stays_in_capture);
 }

@@ -118,6 +118,7 @@ class ProjectedMix(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_y):
+        binding().stays_in_capture()
         codes, scales, H = ctx.saved_tensors
         gx, gH = stream_mix_bwd_ckpt((codes, scales), H, grad_y.contiguous(), format=ctx.format)
         return gx, birkhoff_bwd(H, gH, out=gH), None, None
@@ -126,7 +127,9 @@ class ProjectedMix(torch.autograd.Function):
 def projected_mix(x, logits, *, format="e4m3", **opts):
     """Differentiable stream mix of x [T,4,C] bf16 by the projection of logits
     [T,4,4] fp32.  Keeps H and an 8-bit checkpoint of x; the gradient for the
-    logits is that of the checkpointed x.  ``opts`` are the solver's."""
+    logits is that of the checkpointed x.  ``opts`` are the solver's.  A
+    captured backward raises where it would reach an eager graph on the default
+    stream."""
     return ProjectedMix.apply(x, logits, format, opts)
 
 
@@ -280,7 +283,8 @@ def mx4_linear(x, w, *, format="e4m3"):
     N and K multiples of 32).  Each of the three products takes both operands
     in MXFP4, quantised along the axis it sums over: y = q(x) q(w)^T,
     grad_x = q(gy) q(w^T)^T, grad_w = q(gy^T) q(xhat^T)^T.  x is kept for the
-    backward as an 8-bit checkpoint (xhat), w as it is.  Differentiable once."""
+    backward as an 8-bit checkpoint (xhat), w as it is.  Differentiable once; a captured
+    backward raises where it would reach an eager graph on the default stream."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be [M, K] and [N, K]")
     if any(s % BLOCK for s in (*x.shape, *w.shape)):

@@ -494,7 +494,9 @@ mhc_status mhc_layer_bwd_ckpt(const mhc_layer_args* a, const mhc_layer_ckpt* ckp
  *   scales  [R, C/32] bytes, s standing for 2^(s - 127), 255 for NaN
  * Quantisation takes the scale of a block of 32 as for the checkpoints, with
  * M = 6 and lo = 2, and rounds to the nearest value, ties to the even code.
- * Any scale byte is accepted where a quantised matrix is read. */
+ * Any scale byte is accepted where a quantised matrix is read.  Scales are read
+ * in whole aligned words of 4 bytes: where their number is no multiple of 4, up
+ * to 3 bytes behind the last one are read and not used. */
 
 /* mhc_mx4_quantize -- x [R, C] bf16 or fp32 to MXFP4.
  *   transpose = 0: blocks along the rows; codes [R, C/2], scales [R, C/32];

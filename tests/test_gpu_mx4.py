@@ -237,6 +237,73 @@ def test_linear_strides_and_refusals(gpu_lib):
     assert not gpu_lib.mx4_linear(x, w).requires_grad
 
 
+def test_linear_captured(gpu_lib):
+    """A training step recorded in a graph, its gradients written by value, on
+    every replay what the eager step gives; and inference mode."""
+    x, w, gy = rand((96, 64), 1), rand((160, 64), 2), rand((96, 160), 3)
+    leaves = [t.clone().requires_grad_(True) for t in (x, w)]
+    out = []
+
+    def step():
+        y = gpu_lib.mx4_linear(*leaves)
+        return [y.detach(), *torch.autograd.grad(y, leaves, gy)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k in range(4):
+        with torch.no_grad():
+            leaves[0].copy_(rand((96, 64), 10 + k))
+            leaves[1].copy_(rand((160, 64), 20 + k))
+        gy.copy_(rand((96, 160), 30 + k))
+        graph.replay()
+        got = [t.clone() for t in out]
+        torch.cuda.synchronize()
+        fresh = [t.detach().clone().requires_grad_(True) for t in leaves]
+        y = gpu_lib.mx4_linear(*fresh)
+        want = [y.detach(), *torch.autograd.grad(y, fresh, gy)]
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+    with torch.inference_mode():
+        assert torch.equal(gpu_lib.mx4_linear(*[t.detach().clone() for t in leaves]), want[0])
+
+
+def test_captured_backward_of_an_eager_graph_raises(gpu_lib):
+    """While an eager graph of the same leaves lives, a captured backward is
+    refused in the node before the one it could not reach; without it the same
+    capture goes through."""
+    gy = rand((64, 96), 3)
+    x, w = rand((64, 32), 1).requires_grad_(True), rand((96, 32), 2).requires_grad_(True)
+    xm = rand((4, 4, 64), 4).requires_grad_(True)
+    lg = rand((4, 4, 4), 5, torch.float32).requires_grad_(True)
+    gm = rand((4, 4, 64), 6)
+    cases = [lambda: torch.autograd.grad(gpu_lib.mx4_linear(x, w), (x, w), gy),
+             lambda: torch.autograd.grad(gpu_lib.projected_mix(xm, lg), (xm, lg), gm)]
+    held = [gpu_lib.mx4_linear(x, w), gpu_lib.projected_mix(xm, lg)]
+    torch.cuda.synchronize()
+    for run in cases:
+        graph = torch.cuda.CUDAGraph()
+        with pytest.raises(RuntimeError, match="eager graph"):
+            with torch.cuda.graph(graph):
+                run()
+        torch.cuda.synchronize()
+    del held
+    for run in cases:
+        want = run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run()
+        for _ in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_linear_gradient_by_differences(gpu_lib):
     """With operands that MXFP4 and the checkpoint hold exactly, the map is
     bilinear and a central difference of the loss is its derivative."""
