@@ -6,9 +6,9 @@
 //          sigmoid derivative and projection backward -> grad_logits
 //   dx     grad_x, grad_f
 //   dw     grad_W partials on MFMA
-// The maps of the forward are the layer's read half's (read.hip); the
-// transposition of W and the reduction of the grad_W partials are the plain
-// layer's.
+// The maps of the forward come from the partial sums of the layer's read half
+// (read.hip) or from the plain layer's maps pass, as there; the reduction of
+// the grad_W partials is the plain layer's.
 //
 // The formulas are the plain layer's with xhat, fhat (what the checkpoints
 // stand for) in the place of x, f; the forward's r, logits and maps are those
@@ -22,6 +22,7 @@
 #include "mxfmt.h"
 #include "proj4.h"
 #include "qkernels.h"
+#include "tokenmaps.h"
 #include "wave.h"
 
 namespace mhc {
@@ -82,6 +83,51 @@ MHC_DEV int64_t dl_at(int64_t t, int part, int map)
     return ((t >> 5) * kDlParts + part) * (kMaps * 32) + map * 32 + (t & 31);
 }
 
+// One chunk of 8 columns of token t: u, x_out and both checkpoints from the
+// chunk of x and f.  Quads of lanes are whole (C8 is a multiple of 8).
+template <int FMT>
+MHC_DEV void layer_mix_chunk(const float (&M)[kMaps], const uint4 (&xq)[4], const uint4& fq, int64_t t, int64_t c,
+                             int64_t C8, uint4* __restrict__ u, uint4* __restrict__ xo, uint2* __restrict__ xc,
+                             uint8_t* __restrict__ xs_out, uint2* __restrict__ fc, uint8_t* __restrict__ fs_out)
+{
+    float xs[4][8], ff[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mx_unpack8(xq[j], xs[j]);
+    mx_unpack8(fq, ff);
+    float uu[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float s = M[0] * xs[0][e];
+        s = __builtin_fmaf(M[1], xs[1][e], s);
+        s = __builtin_fmaf(M[2], xs[2][e], s);
+        uu[e] = __builtin_fmaf(M[3], xs[3][e], s);
+    }
+    mhc_store_stream(&u[t * C8 + c], mx_pack8(uu));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float o8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float s = M[4 + i] * ff[e];
+            s = __builtin_fmaf(M[8 + 4 * i + 0], xs[0][e], s);
+            s = __builtin_fmaf(M[8 + 4 * i + 1], xs[1][e], s);
+            s = __builtin_fmaf(M[8 + 4 * i + 2], xs[2][e], s);
+            o8[e] = __builtin_fmaf(M[8 + 4 * i + 3], xs[3][e], s);
+        }
+        mhc_store_stream(&xo[(t * 4 + i) * C8 + c], mx_pack8(o8));
+    }
+    const bool lead = (c & 3) == 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t m = mx_quad_max(mx_amax8(xq[j])), s = mx_scale_byte<FMT>(m);
+        mx_store_stream(&xc[(t * 4 + j) * C8 + c], mx_encode8<FMT>(xs[j], m, s));
+        if (lead) xs_out[(t * 4 + j) * (C8 / 4) + (c >> 2)] = (uint8_t)s;
+    }
+    const uint32_t m = mx_quad_max(mx_amax8(fq)), s = mx_scale_byte<FMT>(m);
+    mx_store_stream(&fc[t * C8 + c], mx_encode8<FMT>(ff, m, s));
+    if (lead) fs_out[t * (C8 / 4) + (c >> 2)] = (uint8_t)s;
+}
+
 // ---------------------------------------------------------------------------
 // mix: read-mix u, write-back x_out and the checkpoints of x and f, 16 tokens
 // per workgroup (spaced by the grid size, so the workgroups stream a
@@ -119,43 +165,44 @@ __global__ __launch_bounds__(kBlock) void layer_mix_ckpt_kernel(
 #pragma unroll
             for (int j = 0; j < 4; ++j) xq[j] = mhc_load_stream(&x[(t * 4 + j) * C8 + c]);
             const uint4 fq = mhc_load_stream(&f[t * C8 + c]);
-            float xs[4][8], ff[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) mx_unpack8(xq[j], xs[j]);
-            mx_unpack8(fq, ff);
-            float uu[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float s = M[0] * xs[0][e];
-                s = __builtin_fmaf(M[1], xs[1][e], s);
-                s = __builtin_fmaf(M[2], xs[2][e], s);
-                uu[e] = __builtin_fmaf(M[3], xs[3][e], s);
-            }
-            mhc_store_stream(&u[t * C8 + c], mx_pack8(uu));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float o8[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float s = M[4 + i] * ff[e];
-                    s = __builtin_fmaf(M[8 + 4 * i + 0], xs[0][e], s);
-                    s = __builtin_fmaf(M[8 + 4 * i + 1], xs[1][e], s);
-                    s = __builtin_fmaf(M[8 + 4 * i + 2], xs[2][e], s);
-                    o8[e] = __builtin_fmaf(M[8 + 4 * i + 3], xs[3][e], s);
-                }
-                mhc_store_stream(&xo[(t * 4 + i) * C8 + c], mx_pack8(o8));
-            }
-            const bool lead = (c & 3) == 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t m = mx_quad_max(mx_amax8(xq[j])), s = mx_scale_byte<FMT>(m);
-                mx_store_stream(&xc[(t * 4 + j) * C8 + c], mx_encode8<FMT>(xs[j], m, s));
-                if (lead) xs_out[(t * 4 + j) * (C8 / 4) + (c >> 2)] = (uint8_t)s;
-            }
-            const uint32_t m = mx_quad_max(mx_amax8(fq)), s = mx_scale_byte<FMT>(m);
-            mx_store_stream(&fc[t * C8 + c], mx_encode8<FMT>(ff, m, s));
-            if (lead) fs_out[t * (C8 / 4) + (c >> 2)] = (uint8_t)s;
+            layer_mix_chunk<FMT>(M, xq, fq, t, c, C8, u, xo, xc, xs_out, fc, fs_out);
         }
+    }
+}
+
+// Where the maps' sums are split (read.hip): a workgroup per token finishes its
+// maps and goes on to the mix, whose first chunks of x and f are under way
+// meanwhile (forward in a graph, us, against maps and mix one after the other:
+// 1 x 7168 15 / 17, 300 x 256 12.5 / 15.3, 4096 x 7168 191 / 213).
+template <int SOLVER, int FMT>
+__global__ __launch_bounds__(kBlock) void layer_finish_ckpt_kernel(
+    const uint4* __restrict__ x, const uint4* __restrict__ f, const float* __restrict__ partial, int splits,
+    TokenMaps maps, uint4* __restrict__ u, uint4* __restrict__ xo, uint2* __restrict__ xc,
+    uint8_t* __restrict__ xs_out, uint2* __restrict__ fc, uint8_t* __restrict__ fs_out, int64_t T, int64_t C8,
+    float eps, SolverOpts opts)
+{
+    __shared__ TokenLds s;
+    __shared__ float sM[kMaps];
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x;
+    uint4 xq[4], fq;
+    const auto load = [&](int64_t c) {
+        c = c < C8 ? c : C8 - 1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xq[j] = mhc_load_stream(&x[(t * 4 + j) * C8 + c]);
+        fq = mhc_load_stream(&f[t * C8 + c]);
+    };
+    load(tid);
+    const float inv = token_logits(s, partial, splits, maps, t, T, C8, eps);
+    if (tid < 8) sM[tid] = token_sigmoid(s.l[tid] * inv);
+    if (tid == 64) token_project<SOLVER>(s, inv, maps, t, opts, &sM[8]);
+    __syncthreads();
+    float M[kMaps];
+#pragma unroll
+    for (int m = 0; m < kMaps; ++m) M[m] = sM[m];
+    for (int64_t c = tid; c < C8; c += kBlock) {
+        if (c != tid) load(c);
+        layer_mix_chunk<FMT>(M, xq, fq, t, c, C8, u, xo, xc, xs_out, fc, fs_out);
     }
 }
 
@@ -299,6 +346,26 @@ struct DotsOut {
     int64_t T, D;  // tokens; D = 4C
 };
 
+// W [24, 4C] transposed, [4C][24], by the workgroups of a dots launch behind
+// those of the tokens: one launch less (the pass over dx wants it next).
+struct WtOut {
+    const uint16_t* W;
+    uint4* Wt;
+    unsigned first;  // workgroup
+};
+
+MHC_DEV void transpose_W(const WtOut& o, int64_t D)
+{
+    const int64_t k = (int64_t)(blockIdx.x - o.first) * kBlock + threadIdx.x;
+    if (k >= D) return;
+    uint4 v[kMaps / 8];
+    uint32_t* w = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+    for (int m = 0; m < kMaps; m += 2) w[m / 2] = o.W[m * D + k] | (uint32_t)o.W[(m + 1) * D + k] << 16;
+#pragma unroll
+    for (int q = 0; q < kMaps / 8; ++q) o.Wt[kMaps / 8 * k + q] = v[q];
+}
+
 // One lane finishes token t (tokens from T on: zeros for the grad_W pass).
 MHC_DEV void finish_token(const DotsOut& o, int64_t t, const float* dots)
 {
@@ -358,8 +425,9 @@ template <int FMT, int W>
 __global__ __launch_bounds__(kBlock) void layer_dots_ckpt_kernel(
     const uint2* __restrict__ xc, const uint8_t* __restrict__ xs, const uint2* __restrict__ fc,
     const uint8_t* __restrict__ fs, const uint4* __restrict__ gxo, const uint4* __restrict__ gu,
-    DotsOut o, int64_t Tp, int64_t C8, int tw)
+    DotsOut o, WtOut wt, int64_t Tp, int64_t C8, int tw)
 {
+    if (blockIdx.x >= wt.first) return transpose_W(wt, o.D);
     const int64_t T = o.T;
     __shared__ float sDots[4][16][kMaps];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -400,8 +468,9 @@ template <int FMT>
 __global__ __launch_bounds__(kBlock) void layer_dots_few_ckpt_kernel(
     const uint2* __restrict__ xc, const uint8_t* __restrict__ xs, const uint2* __restrict__ fc,
     const uint8_t* __restrict__ fs, const uint4* __restrict__ gxo, const uint4* __restrict__ gu,
-    DotsOut o, int64_t C8)
+    DotsOut o, WtOut wt, int64_t C8)
 {
+    if (blockIdx.x >= wt.first) return transpose_W(wt, o.D);
     __shared__ float sDots[4][kMaps];
     __shared__ float sSum[kMaps];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -793,23 +862,21 @@ hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, in
     const uint2* fc = static_cast<const uint2*>(f.codes);
     const uint4* gxo = static_cast<const uint4*>(a.grad_x_out);
     const uint4* gu = static_cast<const uint4*>(a.grad_u);
+    const unsigned extra = (unsigned)((4 * C + kBlock - 1) / kBlock);
+    WtOut wo{(const uint16_t*)a.W, wt, 0};
     if (T <= kFewTokens && C > 512) {
-        hipLaunchKernelGGL(layer_dots_few_ckpt_kernel<FMT>, dim3((unsigned)p.Tp), dim3(kBlock), 0, stream,
-                           xc, x.scales, fc, f.scales, gxo, gu, o, C / 8);
+        wo.first = (unsigned)p.Tp;
+        hipLaunchKernelGGL(layer_dots_few_ckpt_kernel<FMT>, dim3(wo.first + extra), dim3(kBlock), 0, stream,
+                           xc, x.scales, fc, f.scales, gxo, gu, o, wo, C / 8);
     } else {
         int tw = 16;  // tokens per wave: a workgroup for every compute unit where there are as many tokens
         while (tw > (C <= 256 ? 4 : 1) && p.Tp / (4 * tw) < 256) tw /= 2;
-        const dim3 grid((unsigned)(p.Tp / (4 * tw)));
-        if (C <= 256)
-            hipLaunchKernelGGL((layer_dots_ckpt_kernel<FMT, 16>), grid, dim3(kBlock), 0, stream, xc,
-                               x.scales, fc, f.scales, gxo, gu, o, p.Tp, C / 8, tw);
-        else
-            hipLaunchKernelGGL((layer_dots_ckpt_kernel<FMT, 64>), grid, dim3(kBlock), 0, stream, xc,
-                               x.scales, fc, f.scales, gxo, gu, o, p.Tp, C / 8, tw);
+        wo.first = (unsigned)(p.Tp / (4 * tw));
+        auto* dots = C <= 256 ? layer_dots_ckpt_kernel<FMT, 16> : layer_dots_ckpt_kernel<FMT, 64>;
+        hipLaunchKernelGGL(dots, dim3(wo.first + extra), dim3(kBlock), 0, stream, xc, x.scales, fc, f.scales,
+                           gxo, gu, o, wo, p.Tp, C / 8, tw);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    e = launch_layer_wt(a.W, wt, C, stream);
     if (e != hipSuccess) return e;
     // column ranges of whole pairs of chunks, for about 512 workgroups
     const int64_t tiles = (T + kDxTok - 1) / kDxTok, pairs = (C + 2 * kDxChunk - 1) / (2 * kDxChunk);
@@ -823,11 +890,23 @@ hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, in
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(layer_dw_ckpt_kernel<FMT>, dim3((unsigned)(4 * C / (2 * kDwK)), (unsigned)p.groups),
-                       dim3(kBlock), 0, stream, (const uint8_t*)x.codes, x.scales, dlT, partial, T,
-                       p.Tp, C, p.group_tokens);
+                       dim3(kBlock), 0, stream, (const uint8_t*)x.codes, x.scales, dlT,
+                       p.groups == 1 ? a.grad_W : partial, T, p.Tp, C, p.group_tokens);
     e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || p.groups == 1) return e;
     return launch_layer_dw_reduce(partial, a.grad_W, C, p.groups, stream);
+}
+
+template <int FMT>
+hipError_t layer_finish_as(const LayerPtrs& a, const Packed& x, const Packed& f, const ReadPlan& p, int64_t T,
+                           int64_t C, float eps, const SolverOpts& o, hipStream_t stream)
+{
+    const TokenMaps maps{a.logits, a.rms, a.H_pre, a.H_post, a.H_res};
+    auto* kernel = o.solver == 0 ? layer_finish_ckpt_kernel<0, FMT> : layer_finish_ckpt_kernel<1, FMT>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)T), dim3(kBlock), 0, stream, (const uint4*)a.x, (const uint4*)a.f,
+                       static_cast<const float*>(a.workspace), (int)p.splits, maps, (uint4*)a.u, (uint4*)a.x_out,
+                       (uint2*)x.codes, x.scales, (uint2*)f.codes, f.scales, T, C / 8, eps, o);
+    return hipGetLastError();
 }
 
 template <int FMT>
@@ -853,6 +932,7 @@ LayerCkptPlan layer_ckpt_plan(int64_t T, int64_t C)
     // most (their partials are read back); 35928 x 64: 48 us with 16 groups
     int64_t want = 512 / (C / 64);
     want = want < 16 ? 16 : (want > 64 ? 64 : want);
+    if (p.Tp <= 256) want = 1;  // straight to grad_W
     p.group_tokens = ((p.Tp + want - 1) / want + 127) / 128 * 128;
     if (p.group_tokens < 128) p.group_tokens = 128;  // no tokens
     p.groups = (p.Tp + p.group_tokens - 1) / p.group_tokens;
@@ -869,7 +949,14 @@ hipError_t launch_layer_fwd_ckpt(const LayerPtrs& a, const Packed& x, const Pack
                                  int64_t C, float eps, int fmt, const SolverOpts& o,
                                  hipStream_t stream)
 {
-    const hipError_t e = launch_maps(a, T, C, eps, o, stream);
+    const ReadPlan p = read_plan(T, C);
+    if (p.splits != 0) {
+        const hipError_t e = launch_read_part(a, p, T, C, stream);
+        if (e != hipSuccess) return e;
+        return fmt == kE4M3 ? layer_finish_as<kE4M3>(a, x, f, p, T, C, eps, o, stream)
+                            : layer_finish_as<kInt8>(a, x, f, p, T, C, eps, o, stream);
+    }
+    const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
     if (e != hipSuccess) return e;
     return fmt == kE4M3 ? layer_mix_as<kE4M3>(a, x, f, T, C, stream)
                         : layer_mix_as<kInt8>(a, x, f, T, C, stream);

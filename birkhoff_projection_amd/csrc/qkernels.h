@@ -79,9 +79,8 @@ struct ReadPlan {
     int tiles;  // of 16 tokens to a workgroup of the partial sums
 };
 ReadPlan read_plan(int64_t T, int64_t C);
-// The maps alone (the same as launch_layer_read's), with the same workspace.
-hipError_t launch_maps(const LayerPtrs& a, int64_t T, int64_t C, float eps, const SolverOpts& o,
-                       hipStream_t stream);
+// The partial sums of a plan that splits.
+hipError_t launch_read_part(const LayerPtrs& a, const ReadPlan& p, int64_t T, int64_t C, hipStream_t stream);
 hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, int64_t C, float eps,
                              const SolverOpts& o, hipStream_t stream);
 
@@ -89,7 +88,7 @@ hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, in
 // W^T [4C][24] bf16 | grad_W partials [groups][24][4C] fp32 (each 256-byte
 // aligned).
 struct LayerCkptPlan {
-    int64_t Tp, group_tokens, groups;  // as in LayerPlan
+    int64_t Tp, group_tokens, groups;  // tokens padded to 64; groups of the grad_W pass
     int64_t off_s, off_dl, off_wt, off_partial;
     int64_t bytes;
 };

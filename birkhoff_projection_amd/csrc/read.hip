@@ -15,6 +15,7 @@
 #include "mxfmt.h"
 #include "proj4.h"
 #include "qkernels.h"
+#include "tokenmaps.h"
 #include "wave.h"
 
 namespace mhc {
@@ -22,13 +23,10 @@ namespace mhc {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kMaps = 24;
-constexpr int kVals = kMaps + 1;  // logits and the sum of squares
+constexpr int kMaps = kTokenMaps, kVals = kTokenVals;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
-
-MHC_DEV float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
 // u of 8 columns, stored as bf16 and / or MXFP4.  The 4-bit codes are those of
 // the bf16 u, so they do not depend on whether u itself is kept.  Quads of
@@ -174,58 +172,21 @@ __global__ __launch_bounds__(kBlock) void read_part_kernel(const uint16_t* __res
 
 template <int SOLVER>
 __global__ __launch_bounds__(kBlock) void read_finish_kernel(
-    const uint4* __restrict__ x, const float* __restrict__ partial, int splits,
-    float* __restrict__ logits, float* __restrict__ rms, float* __restrict__ Hpre,
-    float* __restrict__ Hpost, float* __restrict__ Hres, UOut o, int64_t T, int64_t C8, float eps,
-    SolverOpts opts)
+    const uint4* __restrict__ x, const float* __restrict__ partial, int splits, TokenMaps maps, UOut o,
+    int64_t T, int64_t C8, float eps, SolverOpts opts)
 {
-    __shared__ float sP[8][32];
-    __shared__ float sL[kVals];
+    __shared__ TokenLds s;
     const int tid = threadIdx.x;
     const int64_t t = blockIdx.x;
-    {
-        const int m = tid & 31, g = tid >> 5;
-        float s = 0.f;
-        if (m < kVals)
-            for (int k = g; k < splits; k += 8) s += partial[((int64_t)k * T + t) * kVals + m];
-        sP[g][m] = s;
-    }
-    __syncthreads();
-    if (tid < kVals) {
-        float s = 0.f;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) s += sP[g][tid];
-        sL[tid] = s;
-    }
-    __syncthreads();
-    const float r = sqrtf(sL[kMaps] / (float)(32 * C8) + eps);
-    const float inv = 1.f / r;
-    if (tid < kMaps) {
-        const float l = sL[tid] * inv;
-        logits[kMaps * t + tid] = l;
-        if (tid == 0) rms[t] = r;
-        if (tid < 4) Hpre[4 * t + tid] = sigmoid(l);
-        else if (tid < 8) Hpost[4 * t + tid - 4] = sigmoid(l);
-    }
+    const float inv = token_logits(s, partial, splits, maps, t, T, C8, eps);
     if (tid < 64) {  // wave 0: the projection (one lane), the others go on to u
-        if (tid == 0) {
-            float a[16], h[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) a[k] = sL[8 + k] * inv;
-            if (SOLVER == 0)
-                project_newton(a, h, opts);
-            else
-                project_sinkhorn(a, h, opts);
-            float4* ho = reinterpret_cast<float4*>(Hres + 16 * t);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ho[q] = make_float4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
-        }
+        float h[16];
+        if (tid == 0) token_project<SOLVER>(s, inv, maps, t, opts, h);
         return;
     }
-    if (o.u == nullptr && o.codes == nullptr) return;  // the maps alone
     float M[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) M[j] = sigmoid(sL[j] * inv);
+    for (int j = 0; j < 4; ++j) M[j] = token_sigmoid(s.l[j] * inv);
     for (int64_t c = tid - 64; c < C8; c += kBlock - 64) {
         uint4 xq[4];
 #pragma unroll
@@ -259,34 +220,14 @@ ReadPlan read_plan(int64_t T, int64_t C)
     return p;
 }
 
-// Few tokens: maps, and u where `uo` has a place for it.
-static hipError_t launch_split(const LayerPtrs& a, const ReadPlan& p, const UOut& uo, int64_t T,
-                               int64_t C, float eps, const SolverOpts& o, hipStream_t stream)
+hipError_t launch_read_part(const LayerPtrs& a, const ReadPlan& p, int64_t T, int64_t C, hipStream_t stream)
 {
-    float* partial = static_cast<float*>(a.workspace);
     const int64_t tok = kPartTok * p.tiles;
     auto* part = p.tiles == 4 ? read_part_kernel<4> : read_part_kernel<1>;
     hipLaunchKernelGGL(part, dim3((unsigned)((T + tok - 1) / tok), (unsigned)p.splits), dim3(kBlock), 0,
-                       stream, (const uint16_t*)a.x, (const uint16_t*)a.W, partial, T, 4 * C, p.steps_per);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (o.solver == 0)
-        hipLaunchKernelGGL(read_finish_kernel<0>, dim3((unsigned)T), dim3(kBlock), 0, stream,
-                           (const uint4*)a.x, partial, (int)p.splits, a.logits, a.rms, a.H_pre,
-                           a.H_post, a.H_res, uo, T, C / 8, eps, o);
-    else
-        hipLaunchKernelGGL(read_finish_kernel<1>, dim3((unsigned)T), dim3(kBlock), 0, stream,
-                           (const uint4*)a.x, partial, (int)p.splits, a.logits, a.rms, a.H_pre,
-                           a.H_post, a.H_res, uo, T, C / 8, eps, o);
+                       stream, (const uint16_t*)a.x, (const uint16_t*)a.W, static_cast<float*>(a.workspace), T,
+                       4 * C, p.steps_per);
     return hipGetLastError();
-}
-
-hipError_t launch_maps(const LayerPtrs& a, int64_t T, int64_t C, float eps, const SolverOpts& o,
-                       hipStream_t stream)
-{
-    const ReadPlan p = read_plan(T, C);
-    if (p.splits == 0) return launch_layer_maps(a, T, C, eps, o, stream);
-    return launch_split(a, p, UOut{nullptr, nullptr, nullptr}, T, C, eps, o, stream);
 }
 
 hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, int64_t C, float eps,
@@ -294,7 +235,15 @@ hipError_t launch_layer_read(const LayerPtrs& a, const Packed& u4, int64_t T, in
 {
     const UOut uo{(uint4*)a.u, (uint32_t*)u4.codes, u4.scales};
     const ReadPlan p = read_plan(T, C);
-    if (p.splits != 0) return launch_split(a, p, uo, T, C, eps, o, stream);
+    if (p.splits != 0) {
+        const hipError_t e = launch_read_part(a, p, T, C, stream);
+        if (e != hipSuccess) return e;
+        const TokenMaps maps{a.logits, a.rms, a.H_pre, a.H_post, a.H_res};
+        auto* finish = o.solver == 0 ? read_finish_kernel<0> : read_finish_kernel<1>;
+        hipLaunchKernelGGL(finish, dim3((unsigned)T), dim3(kBlock), 0, stream, (const uint4*)a.x,
+                           static_cast<const float*>(a.workspace), (int)p.splits, maps, uo, T, C / 8, eps, o);
+        return hipGetLastError();
+    }
     const hipError_t e = launch_layer_maps(a, T, C, eps, o, stream);
     if (e != hipSuccess) return e;
     const int shift = token_shift(C / 8);
