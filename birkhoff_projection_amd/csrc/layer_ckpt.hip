@@ -7,8 +7,7 @@
 //   dx     grad_x, grad_f
 //   dw     grad_W partials on MFMA
 // The maps of the forward come from the partial sums of the layer's read half
-// (read.hip) or from the plain layer's maps pass, as there; the reduction of
-// the grad_W partials is the plain layer's.
+// (read.hip) or from the plain layer's maps pass, as there.
 //
 // The formulas are the plain layer's with xhat, fhat (what the checkpoints
 // stand for) in the place of x, f; the forward's r, logits and maps are those
@@ -74,8 +73,8 @@ MHC_DEV void project_bwd_refined(const float* P, const float* G, float* dA)
 
 // dl / r as an MFMA operand: bf16 parts of 32 tokens' maps,
 // [T / 32][part][map][32 tokens].  The tokens of one product step lie
-// together: with whole rows of tokens per map, 16384 tokens put every map of
-// a step on the same L2 channel (grad_W pass at C = 7168: 186 us, so 167).
+// together: one chunk is one run of bytes, and with whole rows of tokens per map
+// 16384 tokens put every map of a step on the same L2 channel.
 constexpr int kDlParts = 3;
 
 MHC_DEV int64_t dl_at(int64_t t, int part, int map)
@@ -701,69 +700,78 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
 }
 
 // ---------------------------------------------------------------------------
-// dw: workgroup = 256 flattened k x one token group; two waves take one half
-// of the columns each, and every 2nd 32-token chunk of the group:
+// dw: workgroup = 512 flattened k x one token group, a wave 128 of them:
 //   dW^T tile (32 maps x 16 k) += dlT (32 maps x 32 tokens) * xhat (32 tokens x 16 k)
+// Chunks of 32 tokens are copied straight from memory to LDS, two chunks ahead
+// (with the loads in registers, one ahead, two waves per SIMD did not hide
+// them: 16384 x 7168 162 us, so 112, the codes at 4.2 TB/s): a wave its own columns' codes and scales, all four the chunk's dlT,
+// which lies together.  One barrier per chunk.
+//
 // The MFMA B operand wants 8 consecutive tokens of one k per lane, the memory
-// holds 8 consecutive k of one token.  A lane loads 8 k of 8 tokens (16 lanes
-// cover a token's 128 contiguous bytes), decodes them to bf16 and transposes
-// the 8 x 8 square in its own registers, two tokens at a time by byte
-// permutes; MFMA tile nt then holds k = 8 (lane % 16) + nt instead of
-// 16 consecutive k, which only relabels the columns of the result.  So the
-// tile never passes through LDS.  The three bf16 parts of dlT (A, from L2)
-// are issued with the codes, one chunk ahead, into the other of two register
-// sets.  The two partials of each column are summed in LDS and one partial per
-// token group is written, in a fixed order throughout.
+// holds 8 consecutive k of one token.  A lane reads 8 k of 8 tokens, decodes
+// them to bf16 and transposes the 8 x 8 square in its own registers, two tokens
+// at a time by byte permutes; MFMA tile nt then holds k = 8 (lane % 16) + nt
+// instead of 16 consecutive k, which only relabels the columns of the result.
+// One partial per token group is written, in a fixed order throughout.
 // ---------------------------------------------------------------------------
-constexpr int kDwK = 128;         // flattened k per wave, half a workgroup's
+constexpr int kDwK = 128;         // flattened k per wave
 constexpr int kDwNt = kDwK / 16;  // MFMA tiles
+constexpr int kDwStages = 3;
+constexpr int kDlBytes = kDlParts * kMaps * 32 * 2;  // dlT of a chunk
 
-struct DwLoads {
-    uint4 a[kDlParts][2];  // dlT parts: maps 16 mt + row, tokens 8 kq ..+7
-    uint2 x[8];            // codes of token 8 kq + e, k 8 row ..+7
-    uint32_t s[8];
+struct DwStage {
+    uint8_t x[4][32 * kDwK];  // a wave's codes: token r at row r ^ (r / 8 % 2), so that the rows
+                              // a read covers (8 apart) fall on different banks
+    uint32_t s[4][64];        // its scale bytes: 4 of a token in a word; half of it is used
+    uint8_t dl[kDlBytes];
 };
 
-// tc is wave-uniform: every load is a scalar base plus a 32-bit lane offset (at
-// most 31 rows of 2^26 bytes), which keeps 64-bit sums off the vector unit.
-MHC_DEV void dw_issue(DwLoads& d, const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
-                      const __bf16* __restrict__ dlT, int64_t tc, int64_t T, int64_t Tp, int64_t D,
-                      int64_t k0, int lane)
+// One copy of 16 (4) bytes per lane from a wave-uniform base plus a lane offset
+// to a wave-uniform LDS address plus 16 (4) bytes per lane; assembly, because
+// the compiler would wait for all copies before every LDS read.  The wait is
+// the vmcnt before the barrier that hands the stage over.
+MHC_DEV void dw_copy16(const void* base, uint32_t off, uint32_t lds)
 {
-    const int row = lane & 15, kq = lane >> 4;
-    // chunks past the group read a clamped chunk and are not accumulated
-    const int64_t ta = tc + 32 < Tp ? tc : Tp - 32;
-    const __bf16* ab = dlT + dl_at(ta, 0, 0);
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-        const uint32_t m = 16 * mt + row < kMaps ? 16 * mt + row : kMaps - 1;
-#pragma unroll
-        for (int p = 0; p < kDlParts; ++p)
-            d.a[p][mt] = *reinterpret_cast<const uint4*>(ab + p * (kMaps * 32) + (32u * m + 8u * kq));
-    }
-    const int64_t tb = tc < T ? tc : T - 1;
-    const uint8_t* cb = xc + tb * D + k0;
-    const uint8_t* sb = xs + (tb * D + k0) / 32;
-    const int last = (int)(T - tb < 32 ? T - tb : 32) - 1 - 8 * kq;  // e of the lane's last token, below 0 if none
-    const uint32_t cD = (uint32_t)D, sD = cD / 32, r0 = 8u * kq;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t co = e <= last ? r0 * cD + e * cD : (r0 + last) * cD;
-        const uint32_t so = e <= last ? r0 * sD + e * sD : (r0 + last) * sD;
-        d.x[e] = *reinterpret_cast<const uint2*>(cb + (co + 8u * row));
-        d.s[e] = sb[so + row / 4u];
-    }
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(lds), "v"(off), "s"(base) : "memory");
+}
+MHC_DEV void dw_copy4(const void* base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
 
 template <int FMT>
-MHC_DEV void dw_consume(const DwLoads& d, floatx4 (&acc)[2][kDwNt], bool live)
+MHC_DEV void dw_consume(const DwStage& st, int w, int lane, floatx4 (&acc)[2][kDwNt])
 {
-    if (!live) return;
+    const int row = lane & 15, kq = lane >> 4;
+    uint2 x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = *reinterpret_cast<const uint2*>(&st.x[w][((8 * kq + e) ^ (kq & 1)) * kDwK + 8 * row]);
+    uint32_t sc[8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint4 v = *reinterpret_cast<const uint4*>(&st.s[w][8 * kq + 4 * q]);
+        sc[4 * q] = v.x;
+        sc[4 * q + 1] = v.y;
+        sc[4 * q + 2] = v.z;
+        sc[4 * q + 3] = v.w;
+    }
+    bf16x8 a[kDlParts][2];  // maps 16 mt + row, tokens 8 kq ..+7
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+        const int m = 16 * mt + row < kMaps ? 16 * mt + row : kMaps - 1;
+#pragma unroll
+        for (int p = 0; p < kDlParts; ++p)
+            a[p][mt] = as_bf16x8(*reinterpret_cast<const uint4*>(&st.dl[p * (kMaps * 64) + m * 64 + 16 * kq]));
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // 4 of the lane's 8 columns
         uint2 v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = mx_decode4_bf16<FMT>(h ? d.x[e].y : d.x[e].x, mx_scale(d.s[e]));
+        for (int e = 0; e < 8; ++e)
+            v[e] = mx_decode4_bf16<FMT>(h ? x[e].y : x[e].x, mx_scale((sc[e] >> (8 * (row >> 2))) & 0xffu));
         bf16x8 bb[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -783,8 +791,8 @@ MHC_DEV void dw_consume(const DwLoads& d, floatx4 (&acc)[2][kDwNt], bool live)
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt)
-                    acc[mt][4 * h + q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        as_bf16x8(d.a[p][mt]), bb[q], acc[mt][4 * h + q], 0, 0, 0);
+                    acc[mt][4 * h + q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[p][mt], bb[q], acc[mt][4 * h + q],
+                                                                                0, 0, 0);
     }
 }
 
@@ -793,35 +801,62 @@ __global__ __launch_bounds__(kBlock) void layer_dw_ckpt_kernel(
     const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs, const __bf16* __restrict__ dlT,
     float* __restrict__ partial, int64_t T, int64_t Tp, int64_t C, int64_t group_tokens)
 {
-    __shared__ __attribute__((aligned(16))) float sR[4][kMaps][kDwK + 4];
+    __shared__ __attribute__((aligned(16))) DwStage sS[kDwStages];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kq = lane >> 4;
     const int64_t D = 4 * C;
-    const int half = w & 1, phase = w >> 1;
-    const int64_t k0 = (int64_t)blockIdx.x * (2 * kDwK) + kDwK * half;
-    const int64_t g = blockIdx.y;
-    const int64_t tg0 = g * group_tokens;
-    int64_t tg1 = tg0 + group_tokens;
-    if (tg1 > Tp) tg1 = Tp;
+    // waves past the width copy its last columns and store nothing
+    const int64_t kw = (int64_t)blockIdx.x * (4 * kDwK) + kDwK * w, k0 = kw < D ? kw : D - kDwK;
+    const int64_t g = blockIdx.y, tg0 = g * group_tokens;
+    const int64_t tg1 = tg0 + group_tokens < Tp ? tg0 + group_tokens : Tp;
+    const int chunks = (int)((tg1 - tg0) / 32);
+    const uint32_t cD = (uint32_t)D, sD = cD / 32;
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)&sS[0]);
+    constexpr int kCopies = 7;  // per wave and chunk
+    // (chunks past the group's last one repeat it and are not used)
+    const auto copy = [&](int ci, int buf) {
+        const int64_t tc = tg0 + 32 * (int64_t)(ci < chunks ? ci : chunks - 1);
+        // tokens past the last one repeat it: their dlT is zero
+        const int64_t tb = tc < T ? tc : T - 1;
+        const int last = (int)(T - tb < 32 ? T - tb : 32) - 1;
+        const uint32_t at = lds + (uint32_t)sizeof(DwStage) * buf;
+        const uint8_t* cb = xc + tb * D + k0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 8 tokens each
+            int r = (8 * i + (lane >> 3)) ^ (i & 1);
+            r = r < last ? r : last;
+            dw_copy16(cb, (uint32_t)r * cD + 16u * (lane & 7), at + 32 * kDwK * w + 1024 * i);
+        }
+        int r = lane & 31;
+        r = r < last ? r : last;
+        dw_copy4(xs + (tb * D + k0) / 32, (uint32_t)r * sD, at + (uint32_t)offsetof(DwStage, s) + 256 * w);
+        const uint8_t* db = reinterpret_cast<const uint8_t*>(dlT + dl_at(tc, 0, 0));
+        const uint32_t dl = at + (uint32_t)offsetof(DwStage, dl);
+        dw_copy16(db, 16u * (64 * w + lane), dl + 1024 * w);
+        // the last 512 bytes; every wave, so that all count the same copies
+        if (lane < 32) dw_copy16(db, 16u * (256 + lane), dl + 4096);
+    };
+    static_assert(kDlBytes == 4096 + 512, "dlT is copied by 4 waves and half a wave");
     floatx4 acc[2][kDwNt];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int nt = 0; nt < kDwNt; ++nt) acc[mt][nt] = floatx4{0.f, 0.f, 0.f, 0.f};
-    DwLoads d0, d1;
-    const int64_t first = tg0 + 32 * phase;
-    dw_issue(d0, xc, xs, dlT, first, T, Tp, D, k0, lane);
-    for (int64_t tc = first; tc < tg1; tc += 128) {
-        dw_issue(d1, xc, xs, dlT, tc + 64, T, Tp, D, k0, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        dw_consume<FMT>(d0, acc, true);
-        __builtin_amdgcn_sched_barrier(0);
-        dw_issue(d0, xc, xs, dlT, tc + 128, T, Tp, D, k0, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        dw_consume<FMT>(d1, acc, tc + 64 < tg1);
-        __builtin_amdgcn_sched_barrier(0);
+    copy(0, 0);
+    copy(1, 1);
+    int buf = 0;
+    for (int ci = 0; ci < chunks; ++ci) {
+        // this chunk landed (the next one's copies may be under way), and
+        // everybody has read the chunk before, whose buffer is next
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(kCopies) : "memory");
+        copy(ci + 2, buf == 0 ? 2 : buf - 1);
+        dw_consume<FMT>(sS[buf], w, lane, acc);
+        buf = buf == 2 ? 0 : buf + 1;
     }
-    // the two partials of each column, summed in order
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no copy outlives the workgroup
+    if (kw >= D) return;
+    float* out = partial + g * (int64_t)kMaps * D + k0 + 8 * row;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -830,19 +865,35 @@ __global__ __launch_bounds__(kBlock) void layer_dw_ckpt_kernel(
             if (m < kMaps) {
 #pragma unroll
                 for (int nt = 0; nt < kDwNt; nt += 4)
-                    *reinterpret_cast<floatx4*>(&sR[w][m][8 * row + nt]) =
+                    *reinterpret_cast<floatx4*>(&out[m * D + nt]) =
                         floatx4{acc[mt][nt][v], acc[mt][nt + 1][v], acc[mt][nt + 2][v], acc[mt][nt + 3][v]};
             }
         }
-    __syncthreads();
-    float* out = partial + g * (int64_t)kMaps * D;
-    for (int p = threadIdx.x; p < kMaps * 2 * kDwK / 4; p += kBlock) {
-        const int m = p / (2 * kDwK / 4), kk = 4 * (p % (2 * kDwK / 4));
-        const int h = kk / kDwK, c = kk % kDwK;
-        const floatx4 s = *reinterpret_cast<const floatx4*>(&sR[h][m][c]) +
-                          *reinterpret_cast<const floatx4*>(&sR[2 + h][m][c]);
-        *reinterpret_cast<floatx4*>(&out[m * D + (int64_t)blockIdx.x * (2 * kDwK) + kk]) = s;
+}
+
+// grad_W from the partials: 4 threads to 4 columns, each a quarter of the
+// groups, in a fixed order.
+__global__ __launch_bounds__(kBlock) void layer_dw_sum_kernel(const float4* __restrict__ partial,
+                                                              float4* __restrict__ gW, int64_t n4, int groups)
+{
+    __shared__ float4 sQ[4][64];
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int64_t i = (int64_t)blockIdx.x * 64 + lane;  // n4 is a multiple of 64
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int g = q; g < groups; g += 4) {
+        const float4 v = partial[g * n4 + i];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
     }
+    sQ[q][lane] = s;
+    __syncthreads();
+    if (q > 0) return;
+    const float4 a = sQ[0][lane], b = sQ[1][lane], c = sQ[2][lane], d = sQ[3][lane];
+    gW[i] = make_float4((a.x + b.x) + (c.x + d.x), (a.y + b.y) + (c.y + d.y), (a.z + b.z) + (c.z + d.z),
+                        (a.w + b.w) + (c.w + d.w));
 }
 
 constexpr int64_t kFewTokens = 2048;
@@ -889,12 +940,15 @@ hipError_t layer_bwd_as(const LayerPtrs& a, const Packed& x, const Packed& f, in
                        a.grad_logits, svec, (uint4*)a.grad_x, (uint4*)a.grad_f, T, C, per);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(layer_dw_ckpt_kernel<FMT>, dim3((unsigned)(4 * C / (2 * kDwK)), (unsigned)p.groups),
+    hipLaunchKernelGGL(layer_dw_ckpt_kernel<FMT>, dim3((unsigned)((4 * C + 4 * kDwK - 1) / (4 * kDwK)), (unsigned)p.groups),
                        dim3(kBlock), 0, stream, (const uint8_t*)x.codes, x.scales, dlT,
                        p.groups == 1 ? a.grad_W : partial, T, p.Tp, C, p.group_tokens);
     e = hipGetLastError();
     if (e != hipSuccess || p.groups == 1) return e;
-    return launch_layer_dw_reduce(partial, a.grad_W, C, p.groups, stream);
+    const int64_t n4 = kMaps * C;  // of 4 columns
+    hipLaunchKernelGGL(layer_dw_sum_kernel, dim3((unsigned)(n4 / 64)), dim3(kBlock), 0, stream,
+                       (const float4*)partial, (float4*)a.grad_W, n4, (int)p.groups);
+    return hipGetLastError();
 }
 
 template <int FMT>
@@ -927,14 +981,14 @@ LayerCkptPlan layer_ckpt_plan(int64_t T, int64_t C)
 {
     LayerCkptPlan p;
     p.Tp = layer_plan(T, C).Tp;
-    // token groups of the grad_W pass: with C / 64 workgroups to a group, about
-    // 512 in all, but 16 groups at least (the tail is then short) and 64 at
-    // most (their partials are read back); 35928 x 64: 48 us with 16 groups
-    int64_t want = 512 / (C / 64);
-    want = want < 16 ? 16 : (want > 64 ? 64 : want);
+    // token groups of the grad_W pass: one round of workgroups, two to a
+    // compute unit, but 64 groups at most (their partials are read back)
+    const int64_t columns = (4 * C + 4 * kDwK - 1) / (4 * kDwK);
+    int64_t want = 512 / columns;
+    want = want < 1 ? 1 : (want > 64 ? 64 : want);
     if (p.Tp <= 256) want = 1;  // straight to grad_W
-    p.group_tokens = ((p.Tp + want - 1) / want + 127) / 128 * 128;
-    if (p.group_tokens < 128) p.group_tokens = 128;  // no tokens
+    p.group_tokens = ((p.Tp + want - 1) / want + 63) / 64 * 64;
+    if (p.group_tokens < 64) p.group_tokens = 64;  // no tokens
     p.groups = (p.Tp + p.group_tokens - 1) / p.group_tokens;
     const int64_t D = 4 * C;
     p.off_s = 0;
