@@ -202,6 +202,11 @@ def test_linear_wanted_gradients(gpu_lib):
     gx, gw = torch.autograd.grad(gpu_lib.mx4_linear(xr, wr), (xr, wr), gy)
     assert torch.equal(torch.autograd.grad(gpu_lib.mx4_linear(xr, w), xr, gy)[0], gx)
     assert torch.equal(torch.autograd.grad(gpu_lib.mx4_linear(x, wr), wr, gy)[0], gw)
+    a = rand((96, 64), 4).requires_grad_(True)  # one tensor in both places
+    p, q = (a.detach().clone().requires_grad_(True) for _ in range(2))
+    ga = torch.autograd.grad(gpu_lib.mx4_linear(a, a), a, gy[:, :96].contiguous())[0]
+    gp, gq = torch.autograd.grad(gpu_lib.mx4_linear(p, q), (p, q), gy[:, :96].contiguous())
+    assert torch.equal(ga, gp + gq)
     x0 = x[:0].clone().requires_grad_(True)
     g0, w0 = torch.autograd.grad(gpu_lib.mx4_linear(x0, wr).sum(), (x0, wr))
     assert g0.shape == (0, 64) and not bool(w0.any())
