@@ -6,6 +6,8 @@
 // the 32 elements (16 bytes) of row l % 32, block l / 32, and one byte of a
 // register as that block's scale.  Products of two e2m1 elements are exact,
 // the accumulation is fp32.
+#include <type_traits>
+
 #include "mxfmt.h"
 #include "qkernels.h"
 
@@ -113,7 +115,15 @@ MHC_DEV void store8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 // into the freed buffer, between that step's products.  The barrier waits for
 // the next stage's copies only (the counter retires in order).
 //
-// TAIL: K is no multiple of 64 KS.  The last stage's pieces past K repeat the
+// Scales.  A row's scale bytes lie K / 32 apart from the next row's, so every
+// lane of a copy fetches from a line of its own, however little it takes: with
+// a word per lane, two words of each row a stage, the scales cost as many line
+// look-ups as the codes (8192 x 8192 x 4096 in tiles of 256 155 us, of 128 244;
+// with the same words from one line, a test, 138 and 195).  Where K is a
+// multiple of 512 (kPairs) a lane takes the 16 bytes of two stages at once, a
+// quarter of the look-ups.  kWordwise: K is another multiple of 256.
+//
+// kTail: K is no multiple of 64 KS.  The last stage's pieces past K repeat the
 // row's last piece; scale bytes of 0 in both operands make them 2^-254 times
 // their product of at most 32 * 36, which is nothing to a sum in 32 bits.
 // Rows of scales may then start at any byte: the aligned words around a row's
@@ -190,9 +200,13 @@ MHC_DEV void mma_step(const Frags<TM, TN>& f, const Scales<W, TM, TN>& x, f32x16
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int TM, int TN, int WM, int WN, int KS, int NBUF, int EPI, bool TAIL>
+enum Mx4Scales : int { kPairs = 0, kWordwise = 1, kTail = 2 };
+
+template <int TM, int TN, int WM, int WN, int KS, int NBUF, int EPI, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsigned gm, unsigned gn)
 {
+    constexpr bool TAIL = MODE == kTail, PAIRS = MODE == kPairs;
+    static_assert(!PAIRS || KS == 4, "16 scale bytes are two stages of 256");
     constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, ROWS = BM + BN;
     constexpr int kRowBytes = 32 * KS, kRowBlocks = 2 * KS;
     constexpr int kWords = KS / 2, kCopied = TAIL ? kWords + 1 : kWords;  // scale words of a row
@@ -203,7 +217,8 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
     static_assert(WM * WN * 32 * kPitch * 4 + BM * 80 <= NBUF * kBytes,
                   "output strips and maps fit the stage buffers");
     __shared__ __attribute__((aligned(16))) uint8_t sC[NBUF][kBytes];
-    __shared__ uint32_t sX[NBUF][kCopied][ROWS];
+    __shared__ uint32_t sX[PAIRS ? 1 : NBUF][PAIRS ? 1 : kCopied][PAIRS ? 1 : ROWS];
+    __shared__ uint4 sP[2][PAIRS ? ROWS : 1];      // a row's scales of two stages
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // Workgroups go to the 8 dies in turn; each die takes a run of
     // consecutive tiles, in bands of 4 tile rows, so that the rows and columns
@@ -284,7 +299,12 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
     }
     const uint32_t ldsC = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sC[0][0];
     const uint32_t ldsX = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint32_t*)&sX[0][0];
-    constexpr int NC = NA + NB + kCopied * NX;      // copies per thread and stage
+    constexpr int NC = NA + NB + (PAIRS ? 0 : kCopied * NX);  // copies per thread and stage
+    const uint32_t ldsP = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint4*)&sP[0][0];
+    // kPairs: scales of stages st and st + 1 (st even) to the pair's buffer
+    const auto copy_pair = [&](int st, int pair, int x) {
+        copy16_to_lds(baseX[x], offX[x] + (uint32_t)st * kRowBlocks, ldsP + 16 * ((pair & 1) * ROWS + rowX[x]));
+    };
     const auto copy = [&](int st, int buf, int i) {  // copy i of stage st
         if (i < NA + NB) {
             const uint32_t cut = TAIL && st == stages - 1 ? cutLast : 0u;
@@ -304,7 +324,26 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
     // one block, which keeps the products between the copies (the compiler
     // sinks them past a branch, and then nothing overlaps).
     const auto clamped = [&](int st) { return st < stages ? st : stages - 1; };
-    const auto scales = [&](Scales<kCopied, TM, TN>& y, int buf) {
+    const auto scales = [&](Scales<kCopied, TM, TN>& y, int buf, int st) {
+        if constexpr (PAIRS) {
+            const auto two = [&](int row) {
+                return *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(&sP[(st >> 1) & 1][row]) +
+                                                       8 * (st & 1));
+            };
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const uint2 v = two(ra + 32 * i);
+                y.a[0][i] = v.x;
+                y.a[1][i] = v.y;
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const uint2 v = two(BM + rb + 32 * j);
+                y.b[0][j] = v.x;
+                y.b[1][j] = v.y;
+            }
+            return;
+        }
 #pragma unroll
         for (int q = 0; q < kCopied; ++q) {
 #pragma unroll
@@ -330,7 +369,8 @@ return (__builtin_amdgcn_alignbyte(hi, lo, s) >> (8 * kh)) & mask;
             for (int j = 0; j < TN; ++j) x.b[q][j] = pick(y.b[q][j], y.b[q + one][j], sb);
         }
     };
-    // next stage's copies landed, everybody's reads of this one done
+    // next stage's copies landed, everybody's reads of this one done (a stage
+    // that copies a pair's scales too waits for that much more)
     const auto hand_over = [&]() {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"((NBUF - 2) * NC) : "memory");
     };
@@ -351,12 +391,20 @@ return (__builtin_amdgcn_alignbyte(hi, lo, s) >> (8 * kh)) & mask;
         if (b == NBUF - 1) hand_over();  // stage 0 (NBUF - 1 stages are on their way)
 #pragma unroll
         for (int i = 0; i < NC; ++i) copy(clamped(b), b, i);
+        if constexpr (PAIRS) {
+            if (b % 2 == 0) {
+#pragma unroll
+                for (int x = 0; x < NX; ++x) copy_pair(clamped(b) & ~1, b / 2, x);
+            }
+        }
     }
-    scales(y, 0);
+    scales(y, 0, 0);
     shifted(x, y, 0);
     read_frags<KS, 0>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh);
     int buf = 0;
-    for (int st = 0; st < stages; ++st) {
+    const auto stage = [&](int st, auto odd) {
+        constexpr bool kPair = PAIRS && (odd.value + NBUF) % 2 == 0;  // stage st + NBUF begins a pair
+        constexpr int kAll = NC + (kPair ? NX : 0);
         const uint8_t* cA = sC[buf];
         const uint8_t* cB = cA + BM * kRowBytes;
         const int nxt = buf + 1 < NBUF ? buf + 1 : 0;
@@ -370,20 +418,31 @@ return (__builtin_amdgcn_alignbyte(hi, lo, s) >> (8 * kh)) & mask;
         }
         hand_over();
         const uint8_t* nA = sC[nxt];
-        scales(y, nxt);
+        scales(y, nxt, st + 1);
         read_frags<KS, 0>(f0, nA, nA + BM * kRowBytes, ra, rb, kh);
         __builtin_amdgcn_sched_barrier(0);
-        constexpr int kPer = (NC + TM * TN - 1) / (TM * TN);  // copies behind each product
+        constexpr int kPer = (kAll + TM * TN - 1) / (TM * TN);  // copies behind each product
 #pragma unroll
         for (int q = 0; q < TM * TN; ++q) {
             mma_one<KS - 1>(f1, x, acc, q / TN, q % TN);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = kPer * q; i < kPer * (q + 1) && i < NC; ++i) copy(clamped(st + NBUF), buf, i);
+            for (int i = kPer * q; i < kPer * (q + 1) && i < kAll; ++i) {
+                if (i < NC) copy(clamped(st + NBUF), buf, i);
+                else copy_pair(clamped(st + NBUF) & ~1, (st + NBUF) / 2, i - NC);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
         shifted(x, y, st + 1);
         buf = nxt;
+    };
+    if constexpr (PAIRS) {
+        for (int st = 0; st < stages; st += 2) {  // K is a multiple of 512
+            stage(st, std::integral_constant<int, 0>{});
+            stage(st + 1, std::integral_constant<int, 1>{});
+        }
+    } else {
+        for (int st = 0; st < stages; ++st) stage(st, std::integral_constant<int, 0>{});
     }
     // every wave is done with the stage buffers before they hold the outputs
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -656,12 +715,10 @@ void tile_as(const Mx4Args& p, hipStream_t stream)
     constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
     const unsigned gm = (unsigned)((p.M + BM - 1) / BM), gn = (unsigned)((p.N + BN - 1) / BN);
     const dim3 block(64 * WM * WN);
-    if (p.K % (64 * KS) == 0)
-        hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, false>), dim3(gm * gn), block,
-                           0, stream, p, gm, gn);
-    else
-        hipLaunchKernelGGL((mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, true>), dim3(gm * gn), block,
-                           0, stream, p, gm, gn);
+    auto* kernel = p.K % (128 * KS) == 0  ? mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, kPairs>
+                   : p.K % (64 * KS) == 0 ? mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, kWordwise>
+                                          : mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, kTail>;
+    hipLaunchKernelGGL(kernel, dim3(gm * gn), block, 0, stream, p, gm, gn);
 }
 
 // Panels sized for two workgroups per compute unit.
