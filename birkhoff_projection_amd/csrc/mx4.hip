@@ -751,26 +751,27 @@ hipError_t matmul_as(const Mx4Args& p, int src, hipStream_t stream)
     } else if (p.M <= 16 || (p.M + 15) / 16 * ((p.N + 15) / 16) <= 512) {
         // As long as all workgroups of 16 x 16 are on the chip at once (two per
         // compute unit) they beat the tiles below, which then leave most of it
-        // idle (us, against tiles of 64): 32 x 4096, K = 4096 5.5 / 7.4;
-        // 128 x 1024, K = 8192 7.7 / 13.5; but 64 x 4096 (1024 workgroups)
-        // 9.0 / 8.4 and 32 x 7168, K = 7168 (896) 13.2 / 11.2.
+        // idle (us, against tiles of 64): 32 x 4096, K = 4096 5.9 / 7.5;
+        // 128 x 1024, K = 8192 7.7 / 10.0; but 64 x 4096 (1024 workgroups)
+        // 9.0 / 7.2 and 32 x 7168, K = 7168 (896) 13.2 / 9.5.
         few_as<0, EPI>(p, stream);
     } else {
         // Large tiles move the fewest operand bytes per product and win as
         // soon as they cover most of the chip; below that, more tiles.
-        // Measured (us, K = 4096 unless named): 4096 x 4096 (256 tiles of 256)
-        // 45 against 59 with tiles of 128; 2048 x 2048 (64, 256) 29 / 17, 35 with
-        // tiles of 64; 512 x 7168, K = 7168 (56, 224) 55 / 26 / 52; 256 x 4096
-        // (16, 64) 27 / 13 / 9.  Three stage buffers instead of two pay while a
-        // compute unit has one tile (2048 x 2048: 17.3 / 18.8), cost the second
-        // workgroup otherwise (4096 x 4096: 65 / 59).
+        // Measured (us, K = 4096 unless named, tiles of 256 / 128 / 64): 4096 x
+        // 4096 42 / 55 / 84; 4096 x 3584 35 / 44 / 66; 1024 x 7168, K = 7168 (112
+        // tiles of 256) 47 / 37 / 56; 512 x 7168, K = 7168 (224 tiles of 128) 43 /
+        // 21.5 / 33; 512 x 4096 (128) 25 / 12.7 / 11.3; 256 x 4096 (64) 25 / 12 /
+        // 7.7.  Three stage buffers instead of two pay while a compute unit has
+        // one tile (2048 x 2048: 15.5 / 16.5), cost the second workgroup
+        // otherwise (4096 x 4096: 64 / 55).
         const int64_t t256 = ((p.M + 255) / 256) * ((p.N + 255) / 256);
         const int64_t t128 = ((p.M + 127) / 128) * ((p.N + 127) / 128);
         if (t256 >= 192)
             tile_as<2, 4, 4, 2, 4, 2, EPI>(p, stream);
         else if (t128 > 256)
             tile_as<2, 2, 2, 2, 4, 2, EPI>(p, stream);
-        else if (t128 >= 128)
+        else if (t128 > 128)
             tile_as<2, 2, 2, 2, 4, 3, EPI>(p, stream);
         else
             tile_as<1, 1, 2, 2, 4, 3, EPI>(p, stream);
