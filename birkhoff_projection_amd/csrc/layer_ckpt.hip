@@ -130,7 +130,8 @@ MHC_DEV void layer_mix_chunk(const float (&M)[kMaps], const uint4 (&xq)[4], cons
 // ---------------------------------------------------------------------------
 // mix: read-mix u, write-back x_out and the checkpoints of x and f, 16 tokens
 // per workgroup (spaced by the grid size, so the workgroups stream a
-// contiguous front), 2^shift threads to a token.
+// contiguous front), 2^shift threads to a token.  Bound by memory: 16384 x 7168
+// 541-549 us, 5.4 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kMixTokens = 16;
 
@@ -213,7 +214,8 @@ __global__ __launch_bounds__(kBlock) void layer_finish_ckpt_kernel(
 // step i is consumed (the vector-memory counter retires in order), across
 // token boundaries too.  At a token's last chunk the 24 partial dots are
 // wave-reduced into LDS; then lanes 0..tw-1 each finish one token.  Narrow
-// rows (W = 16): 16 lanes to a token, four tokens at a time.
+// rows (W = 16): 16 lanes to a token, four tokens at a time.  Reads only, bound by
+// memory: 16384 x 7168 311-315 us, 5.6 TB/s.
 // ---------------------------------------------------------------------------
 struct DotsLoads {
     uint2 x[4], f;
@@ -512,8 +514,9 @@ __global__ __launch_bounds__(kBlock) void layer_dots_few_ckpt_kernel(
 
 // ---------------------------------------------------------------------------
 // dx: workgroup = 16 tokens x a range of the columns (all of them unless the
-// tokens are few), in chunks of 128 columns of every stream.  Per chunk wave w forms (dl W)^T of stream w on MFMA (16 k x 16
-// tokens, A from the transposed W, B = dl in two bf16 parts, fixed for the
+// tokens are few), in chunks of 128 columns of every stream.  Bound by memory:
+// 16384 x 7168 554-564 us, 5.0 TB/s.  Per chunk wave w forms (dl W)^T of stream
+// w on MFMA (16 k x 16 tokens, A from the transposed W, B = dl in two bf16 parts, fixed for the
 // workgroup) into LDS; then an element-wise pass with lane = (token, 8
 // columns) whose accesses cover 4 rows x 256 contiguous bytes.  All loads of
 // chunk i+1 are issued before chunk i is consumed, into the other of two
