@@ -49,7 +49,9 @@ def close(y, a, b, dtype, label=""):
 SHAPES = [(1, 8, 32), (1, 7168, 4096), (3, 40, 96), (16, 136, 2080), (17, 64, 64), (33, 72, 512), (64, 200, 1056),
           (65, 8, 32), (100, 136, 160), (128, 128, 256), (130, 264, 288), (257, 1000, 480), (640, 4104, 96),
           (2100, 2056, 544), (4352, 4352, 256), (4100, 4360, 800),
-          (130, 1032, 1056), (200, 1000, 512), (40, 2056, 96), (250, 496, 3200)]
+          (130, 1032, 1056), (200, 1000, 512), (40, 2056, 96), (250, 496, 3200),
+          (300, 1032, 2560), (300, 1032, 1280), (1200, 2056, 1024), (1200, 2056, 768), (2100, 2304, 1536),
+          (4352, 4352, 1536), (4352, 4360, 768)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -114,7 +116,8 @@ def test_product_with_itself_and_shared_inputs(gpu_lib):
 
 @pytest.mark.parametrize("T,C,K", [(1, 64, 32), (1, 4096, 4096), (7, 200, 96), (40, 64, 576), (64, 136, 256),
                                    (65, 72, 32), (200, 520, 288), (300, 1024, 512), (2050, 2064, 96), (4100, 4160, 256), (130, 1032, 288),
-                                   (200, 1000, 512), (4100, 4160, 288)])
+                                   (200, 1000, 512), (4100, 4160, 288),
+                                   (300, 1032, 2560), (1200, 2056, 1024), (2100, 2304, 512), (4100, 4160, 1024)])
 def test_write_back(gpu_lib, T, C, K):
     print(f"write back T={T} C={C} K={K}", flush=True)
     a, b = operand(T, K, T), operand(C, K, C)
