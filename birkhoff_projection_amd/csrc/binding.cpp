@@ -54,6 +54,14 @@ Tensor output(const Opt& t, const char* name, at::ScalarType dtype, at::IntArray
     return *t;
 }
 
+// A list from Python of as many tensors as the call takes: its elements are
+// read by their place.
+template <class T>
+void count(const std::vector<T>& v, size_t n, const char* what)
+{
+    TORCH_CHECK_VALUE(v.size() == n, what, ", got ", v.size(), " tensors instead of ", n);
+}
+
 // bf16 or fp32 values; the ABI's dtype code
 int32_t values(const Tensor& t, const char* name)
 {
@@ -247,6 +255,9 @@ std::tuple<int, std::vector<Tensor>, std::vector<Tensor>, std::vector<Tensor>> l
     const Tensor& x, const Tensor& W, const Tensor& f, int32_t format, double eps, const Opts& opts,
     const std::vector<Opt>& maps_out, const std::vector<Opt>& outs, const std::vector<Opt>& ckpt)
 {
+    if (!maps_out.empty()) count(maps_out, 5, "out must hold the 5 maps");
+    count(outs, 2, "out must hold u and x_out");
+    count(ckpt, 4, "ckpt must hold (codes, scales) of x and of f");
     const Shape3 s = streams(x, "x");
     given_W(W, s, x.device());
     given(f, "f", at::kBFloat16, {s.T, s.C}, x.device());
@@ -278,6 +289,9 @@ std::tuple<int, std::vector<Tensor>> layer_bwd_ckpt(
     const Tensor& grad_x_out, const Tensor& grad_u, int32_t format, const Opt& workspace,
     const std::vector<Opt>& outs)
 {
+    count(ckpt, 4, "ckpt must hold (codes, scales) of x and of f");
+    count(maps, 5, "fwd must hold the 5 maps");
+    count(outs, 4, "out must hold the 4 gradients");
     const Shape3 s = streams(grad_x_out, "grad_x_out");
     const at::Device dev = grad_x_out.device();
     const std::vector<int64_t> fs{s.T, s.C};
@@ -326,6 +340,7 @@ std::tuple<int, std::vector<Tensor>, Opt, Opt, Opt> layer_read(
     const Tensor& x, const Tensor& W, bool u4, bool keep_u, double eps, const Opts& opts,
     const std::vector<Opt>& maps_out, const Opt& u_out, const Opt& codes_out, const Opt& scales_out)
 {
+    if (!maps_out.empty()) count(maps_out, 5, "out must hold the 5 maps");
     const Shape3 s = streams(x, "x");
     given_W(W, s, x.device());
     TORCH_CHECK_VALUE(s.C % 2 == 0, "C must be even");
