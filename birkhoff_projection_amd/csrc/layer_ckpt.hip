@@ -18,6 +18,7 @@
 // unrounded.  grad_logits / r enters the grad_W product as three bf16 parts,
 // which hold all 24 bits of an fp32 (its sum over the tokens is then as good
 // as in fp32), and the grad_x product as two, enough for a bf16 result.
+#include "ldscopy.h"
 #include "mxfmt.h"
 #include "proj4.h"
 #include "qkernels.h"
@@ -729,21 +730,6 @@ struct DwStage {
     uint8_t dl[kDlBytes];
 };
 
-// One copy of 16 (4) bytes per lane from a wave-uniform base plus a lane offset
-// to a wave-uniform LDS address plus 16 (4) bytes per lane; assembly, because
-// the compiler would wait for all copies before every LDS read.  The wait is
-// the vmcnt before the barrier that hands the stage over.
-MHC_DEV void dw_copy16(const void* base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory");
-}
-MHC_DEV void dw_copy4(const void* base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory");
-}
-
 template <int FMT>
 MHC_DEV void dw_consume(const DwStage& st, int w, int lane, floatx4 (&acc)[2][kDwNt])
 {
@@ -829,16 +815,16 @@ __global__ __launch_bounds__(kBlock) void layer_dw_ckpt_kernel(
         for (int i = 0; i < 4; ++i) {  // 8 tokens each
             int r = (8 * i + (lane >> 3)) ^ (i & 1);
             r = r < last ? r : last;
-            dw_copy16(cb, (uint32_t)r * cD + 16u * (lane & 7), at + 32 * kDwK * w + 1024 * i);
+            copy16_to_lds(cb, (uint32_t)r * cD + 16u * (lane & 7), at + 32 * kDwK * w + 1024 * i);
         }
         int r = lane & 31;
         r = r < last ? r : last;
-        dw_copy4(xs + (tb * D + k0) / 32, (uint32_t)r * sD, at + (uint32_t)offsetof(DwStage, s) + 256 * w);
+        copy4_to_lds(xs + (tb * D + k0) / 32, (uint32_t)r * sD, at + (uint32_t)offsetof(DwStage, s) + 256 * w);
         const uint8_t* db = reinterpret_cast<const uint8_t*>(dlT + dl_at(tc, 0, 0));
         const uint32_t dl = at + (uint32_t)offsetof(DwStage, dl);
-        dw_copy16(db, 16u * (64 * w + lane), dl + 1024 * w);
+        copy16_to_lds(db, 16u * (64 * w + lane), dl + 1024 * w);
         // the last 512 bytes; every wave, so that all count the same copies
-        if (lane < 32) dw_copy16(db, 16u * (256 + lane), dl + 4096);
+        if (lane < 32) copy16_to_lds(db, 16u * (256 + lane), dl + 4096);
     };
     static_assert(kDlBytes == 4096 + 512, "dlT is copied by 4 waves and half a wave");
     floatx4 acc[2][kDwNt];

@@ -8,6 +8,7 @@
 // the accumulation is fp32.
 #include <type_traits>
 
+#include "ldscopy.h"
 #include "mxfmt.h"
 #include "qkernels.h"
 
@@ -130,23 +131,6 @@ MHC_DEV void store8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 // bytes are copied, one more than it has, and a lane shifts its bytes out of
 // two of them.
 // ---------------------------------------------------------------------------
-
-// One copy of 16 (or 4) bytes per lane from global memory straight to LDS:
-// from a wave-uniform base plus a lane offset to a wave-uniform LDS address
-// plus 16 (4) bytes per lane.  It is written as assembly because the compiler,
-// which cannot tell the buffers apart, would wait for all copies before every
-// LDS read.  It has no register result; the wait is the vmcnt before the
-// barrier that hands the buffer over.
-MHC_DEV void copy16_to_lds(const uint8_t* base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory");
-}
-MHC_DEV void copy4_to_lds(const uint8_t* base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-                 :: "s"(lds), "v"(off), "s"(base) : "memory");
-}
 
 template <int TM, int TN>
 struct Frags {
