@@ -5,9 +5,14 @@ Every HIP source is compiled for gfx950 only, with packed-fp32 code
 generation switched off (``-target-feature -packed-fp32-ops``), then linked
 into one shared library next to this file.  Run ``python -m
 birkhoff_projection_amd.build`` or call :func:`build`.
+
+The C library needs hipcc only: without PyTorch, run this file itself
+(``python birkhoff_projection_amd/build.py``), which then leaves the extension
+module out.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -60,24 +65,14 @@ def binding_link(obj: str, out: str):
             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source and link ``libmhc.so`` and ``_binding.so``; returns
-    the library's path."""
-    cc = hipcc()
-    os.makedirs(BUILD, exist_ok=True)
-    procs = []
-    objs = []
-    bobj = os.path.join(BUILD, "binding.o")
-    procs.append(("binding.cpp", subprocess.Popen(binding_command(bobj), stdout=subprocess.PIPE,
-                                                  stderr=subprocess.STDOUT, text=True)))
-    for src in SOURCES:
-        obj = os.path.join(BUILD, src.replace(".hip", ".o"))
-        objs.append(obj)
-        cmd = [cc] + compile_flags() + ["-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
-                                            stderr=subprocess.STDOUT, text=True)))
+def _start(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _finish(procs, verbose):
+    """Waits for the compilers; the names of the sources that failed."""
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -85,17 +80,51 @@ def build(verbose: bool = False) -> str:
             print(out, end="", file=sys.stderr)
         if p.returncode != 0:
             failed.append(src)
-    if failed:
-        raise RuntimeError(f"compilation failed for {failed}")
-    tmp = LIB + ".tmp"
-    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-Wl,-soname,libmhc.so", "-o", tmp] + objs
+    return failed
+
+
+def _link(cmd, tmp, out, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    tmp = BINDING + ".tmp"
-    subprocess.run(binding_link(bobj, tmp), check=True)
-    os.replace(tmp, BINDING)
+    os.replace(tmp, out)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source and link ``libmhc.so``, then ``_binding.so`` where
+    PyTorch is installed; returns the library's path.  The library is linked
+    whatever becomes of the extension module, whose failure raises afterwards."""
+    cc = hipcc()
+    os.makedirs(BUILD, exist_ok=True)
+    procs = []
+    objs = []
+    for src in SOURCES:
+        obj = os.path.join(BUILD, src.replace(".hip", ".o"))
+        objs.append(obj)
+        procs.append((src, _start([cc] + compile_flags() + ["-c", os.path.join(CSRC, src), "-o", obj],
+                                  verbose)))
+    bobj = os.path.join(BUILD, "binding.o")
+    binding, error = [], None
+    if importlib.util.find_spec("torch") is None:
+        print("no PyTorch: the library alone is built", file=sys.stderr)
+    else:
+        try:
+            binding = [("binding.cpp", _start(binding_command(bobj), verbose))]
+        except Exception as e:  # raised again once the library is linked
+            error = e
+    failed, bfailed = _finish(procs, verbose), _finish(binding, verbose)
+    if failed:
+        raise RuntimeError(f"compilation failed for {failed + bfailed}")
+    tmp = LIB + ".tmp"
+    _link([cc, f"--offload-arch={ARCH}", "-shared", "-Wl,-soname,libmhc.so", "-o", tmp] + objs, tmp, LIB,
+          verbose)
+    if error is not None:
+        raise error
+    if bfailed:
+        raise RuntimeError(f"compilation failed for {bfailed}")
+    if binding:
+        tmp = BINDING + ".tmp"
+        _link(binding_link(bobj, tmp), tmp, BINDING, verbose)
     return LIB
 
 
