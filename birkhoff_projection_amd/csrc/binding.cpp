@@ -17,6 +17,7 @@
 #include <torch/csrc/utils/pybind.h>
 
 #include <tuple>
+#include <unordered_set>
 #include <vector>
 
 #include "../../include/mhc.h"
@@ -521,19 +522,30 @@ std::tuple<int, Tensor> mx4_write_back(const Tensor& ac, const Tensor& as, const
     return {st, std::move(y)};
 }
 
-// Inside a backward that is being captured: does a gradient go on to a node
-// whose stream is the default one, that is, to a graph begun eagerly?  The
-// engine would make that stream wait for the capture, which HIP refuses, and
-// the process ends on it; so the node before it raises instead.
+// Inside a backward that is being captured: does a gradient go on, at once or
+// through nodes in between (a leaf's cast or view), to a node whose stream is
+// the default one, that is, to a graph begun eagerly?  The engine would make
+// that stream wait for the capture, which HIP refuses, and the process ends on
+// it; so the node before it raises instead.  An eager graph begun on another
+// stream joins the capture and is no such case.  Nodes that this backward does
+// not run are passed over.
 bool leaves_capture()
 {
     const auto node = torch::autograd::get_current_node();
     if (node == nullptr || c10::hip::currentStreamCaptureStatusMayInitCtx() != c10::hip::CaptureStatus::Active)
         return false;
-    for (const auto& edge : node->next_edges()) {
-        if (!edge.is_valid()) continue;
-        const auto stream = edge.function->stream();
-        if (stream.has_value() && stream->id() == 0) return true;
+    std::vector<torch::autograd::Node*> todo{node.get()};
+    std::unordered_set<torch::autograd::Node*> seen{node.get()};
+    while (!todo.empty()) {
+        torch::autograd::Node* n = todo.back();
+        todo.pop_back();
+        for (size_t i = 0; i < n->num_outputs(); ++i) {
+            torch::autograd::Node* next = n->next_edge(i).function.get();
+            if (next == nullptr || !n->task_should_compute_output(i) || !seen.insert(next).second) continue;
+            const auto stream = next->stream();
+            if (stream.has_value() && stream->id() == 0) return true;
+            todo.push_back(next);
+        }
     }
     return false;
 }
