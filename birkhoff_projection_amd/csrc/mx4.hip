@@ -99,14 +99,13 @@ MHC_DEV void store8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 
 // ---------------------------------------------------------------------------
 // Tiled product.  Workgroup: WM x WN waves, each 32 TM x 32 TN outputs, K in
-// stages of KS steps of 64 (KS = 4 or 2): 32 KS bytes of codes and 2 KS scale
-// bytes per row.
+// stages of 256, 4 steps of 64: 128 bytes of codes and 8 scale bytes per row.
 //
-// LDS: NBUF stage buffers.  A row is 2 KS pieces of 16 bytes, piece c of row r
-// at place c ^ (r / 2 % 8) (KS = 2: c ^ (r / 4 % 4)): the 16 rows that one phase
-// of a read covers then fall on all 64 banks.  Each 4 scale bytes of a row are one
-// word; a lane of block half h = lane / 32 shifts it by 8 h and finds the
-// scales of two steps in bytes 0 and 2, which the instruction selects.
+// LDS: NBUF stage buffers.  A row is 8 pieces of 16 bytes, piece c of row r at
+// place c ^ (r / 2 % 8): the 16 rows that one phase of a read covers then fall
+// on all 64 banks.  Each 4 scale bytes of a row are one word; a lane of block
+// half h = lane / 32 shifts it by 8 h and finds the scales of two steps in
+// bytes 0 and 2, which the instruction selects.
 //
 // Pipeline: copies run NBUF - 1 stages ahead, straight from global memory to
 // LDS, and two register sets hold fragments: while one step multiplies, the
@@ -124,7 +123,7 @@ MHC_DEV void store8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 // multiple of 512 (kPairs) a lane takes the 16 bytes of two stages at once, a
 // quarter of the look-ups.  kWordwise: K is another multiple of 256.
 //
-// kTail: K is no multiple of 64 KS.  The last stage's pieces past K repeat the
+// kTail: K is no multiple of 256.  The last stage's pieces past K repeat the
 // row's last piece; scale bytes of 0 in both operands make them 2^-254 times
 // their product of at most 32 * 36, which is nothing to a sum in 32 bits.
 // Rows of scales may then start at any byte: the aligned words around a row's
@@ -132,31 +131,35 @@ MHC_DEV void store8(const Mx4Args& p, int64_t m, int64_t n, const float* y)
 // two of them.
 // ---------------------------------------------------------------------------
 
+constexpr int kStageK = 256;                  // of K in a stage
+constexpr int kRowBytes = kStageK / 2;        // codes of a row there
+constexpr int kRowBlocks = kStageK / 32;      // and its scale bytes
+constexpr int kWords = kRowBlocks / 4;
+
 template <int TM, int TN>
 struct Frags {
     uint4 a[TM], b[TN];
 };
 
 // place of piece c of row r
-template <int KS>
 MHC_DEV int piece_at(int r, int c)
 {
-    return KS == 4 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3);
+    return c ^ ((r >> 1) & 7);
 }
 
-template <int KS, int S, int TM, int TN>
+template <int S, int TM, int TN>
 MHC_DEV void read_frags(Frags<TM, TN>& f, const uint8_t* sA, const uint8_t* sB, int ra, int rb,
                         int kh)
 {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int r = ra + 32 * i;
-        f.a[i] = *reinterpret_cast<const uint4*>(sA + r * 32 * KS + 16 * piece_at<KS>(r, 2 * S + kh));
+        f.a[i] = *reinterpret_cast<const uint4*>(sA + r * kRowBytes + 16 * piece_at(r, 2 * S + kh));
     }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
         const int r = rb + 32 * j;
-        f.b[j] = *reinterpret_cast<const uint4*>(sB + r * 32 * KS + 16 * piece_at<KS>(r, 2 * S + kh));
+        f.b[j] = *reinterpret_cast<const uint4*>(sB + r * kRowBytes + 16 * piece_at(r, 2 * S + kh));
     }
 }
 
@@ -186,14 +189,12 @@ MHC_DEV void mma_step(const Frags<TM, TN>& f, const Scales<W, TM, TN>& x, f32x16
 
 enum Mx4Scales : int { kPairs = 0, kWordwise = 1, kTail = 2 };
 
-template <int TM, int TN, int WM, int WN, int KS, int NBUF, int EPI, int MODE>
+template <int TM, int TN, int WM, int WN, int NBUF, int EPI, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsigned gm, unsigned gn)
 {
     constexpr bool TAIL = MODE == kTail, PAIRS = MODE == kPairs;
-    static_assert(!PAIRS || KS == 4, "16 scale bytes are two stages of 256");
     constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, ROWS = BM + BN;
-    constexpr int kRowBytes = 32 * KS, kRowBlocks = 2 * KS;
-    constexpr int kWords = KS / 2, kCopied = TAIL ? kWords + 1 : kWords;  // scale words of a row
+    constexpr int kCopied = TAIL ? kWords + 1 : kWords;  // scale words of a row
     constexpr int kBlock = 64 * WM * WN;
     constexpr int kBytes = ROWS * kRowBytes;       // codes of one stage
     constexpr int TS = TN < 2 ? TN : 2;            // tiles side by side in an output strip
@@ -223,17 +224,17 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
     const int wm = w % WM, wn = w / WM;
     const int ra = 32 * TM * wm + (lane & 31), rb = 32 * TN * wn + (lane & 31);
     const int kh = lane >> 5;
-    const int stages = (int)((p.K + 64 * KS - 1) / (64 * KS));
+    const int stages = (int)((p.K + kStageK - 1) / kStageK);
 
-    // A thread copies piece c of every kStep-th row from tid / (2 KS) on (c and
+    // A thread copies piece c of every kStep-th row from tid / 8 on (c and
     // its place in LDS are fixed by tid).  Rows past the matrix repeat its
     // last one; their products are not used.  Row offsets fit 32 bits: 255
     // rows of at most 2^23 bytes.
-    constexpr int kStep = kBlock / (2 * KS);
+    constexpr int kStep = kBlock / 8;
     constexpr int NA = BM / kStep, NB = BN / kStep;     // code copies per thread and stage
     constexpr int NX = (ROWS + kBlock - 1) / kBlock;    // scale copies
     static_assert(BM % kStep == 0 && BN % kStep == 0 && kStep % 16 == 0, "whole copies, one swizzle per thread");
-    const int row0 = tid / (2 * KS), c16 = 16 * piece_at<KS>(row0, tid % (2 * KS));
+    const int row0 = tid / 8, c16 = 16 * piece_at(row0, tid % 8);
     const uint8_t* baseA = p.a + m0 * Kb;
     const uint8_t* baseB = p.b + n0 * Kb;
     uint32_t offA[NA], offB[NB];
@@ -341,7 +342,7 @@ __global__ __launch_bounds__(64 * WM * WN) void mx4_tile_kernel(Mx4Args p, unsig
         uint32_t mask = 0;
         const auto pick = [&](uint32_t lo, uint32_t hi, uint32_t s) {
             if (!TAIL) return lo >> (8 * kh);
-return (__builtin_amdgcn_alignbyte(hi, lo, s) >> (8 * kh)) & mask;
+            return (__builtin_amdgcn_alignbyte(hi, lo, s) >> (8 * kh)) & mask;
         };
 #pragma unroll
         for (int q = 0; q < kWords; ++q) {
@@ -384,7 +385,7 @@ return (__builtin_amdgcn_alignbyte(hi, lo, s) >> (8 * kh)) & mask;
     }
     scales(y, 0, 0);
     shifted(x, y, 0);
-    read_frags<KS, 0>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh);
+    read_frags<0>(f0, sC[0], sC[0] + BM * kRowBytes, ra, rb, kh);
     int buf = 0;
     const auto stage = [&](int st, auto odd) {
         constexpr bool kPair = PAIRS && (odd.value + NBUF) % 2 == 0;  // stage st + NBUF begins a pair
@@ -392,23 +393,21 @@ return (__builtin_amdgcn_alignbyte(hi, lo, s) >> (8 * kh)) & mask;
         const uint8_t* cA = sC[buf];
         const uint8_t* cB = cA + BM * kRowBytes;
         const int nxt = buf + 1 < NBUF ? buf + 1 : 0;
-        read_frags<KS, 1>(f1, cA, cB, ra, rb, kh);
+        read_frags<1>(f1, cA, cB, ra, rb, kh);
         mma_step<0>(f0, x, acc);
-        if constexpr (KS == 4) {
-            read_frags<KS, 2>(f0, cA, cB, ra, rb, kh);
-            mma_step<1>(f1, x, acc);
-            read_frags<KS, 3>(f1, cA, cB, ra, rb, kh);
-            mma_step<2>(f0, x, acc);
-        }
+        read_frags<2>(f0, cA, cB, ra, rb, kh);
+        mma_step<1>(f1, x, acc);
+        read_frags<3>(f1, cA, cB, ra, rb, kh);
+        mma_step<2>(f0, x, acc);
         hand_over();
         const uint8_t* nA = sC[nxt];
         scales(y, nxt, st + 1);
-        read_frags<KS, 0>(f0, nA, nA + BM * kRowBytes, ra, rb, kh);
+        read_frags<0>(f0, nA, nA + BM * kRowBytes, ra, rb, kh);
         __builtin_amdgcn_sched_barrier(0);
         constexpr int kPer = (kAll + TM * TN - 1) / (TM * TN);  // copies behind each product
 #pragma unroll
         for (int q = 0; q < TM * TN; ++q) {
-            mma_one<KS - 1>(f1, x, acc, q / TN, q % TN);
+            mma_one<3>(f1, x, acc, q / TN, q % TN);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = kPer * q; i < kPer * (q + 1) && i < kAll; ++i) {
@@ -693,15 +692,15 @@ __global__ __launch_bounds__(kFewThreads) void mx4_few_kernel(Mx4Args p, FewShap
     }
 }
 
-template <int TM, int TN, int WM, int WN, int KS, int NBUF, int EPI>
+template <int TM, int TN, int WM, int WN, int NBUF, int EPI>
 void tile_as(const Mx4Args& p, hipStream_t stream)
 {
     constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN;
     const unsigned gm = (unsigned)((p.M + BM - 1) / BM), gn = (unsigned)((p.N + BN - 1) / BN);
     const dim3 block(64 * WM * WN);
-    auto* kernel = p.K % (128 * KS) == 0  ? mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, kPairs>
-                   : p.K % (64 * KS) == 0 ? mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, kWordwise>
-                                          : mx4_tile_kernel<TM, TN, WM, WN, KS, NBUF, EPI, kTail>;
+    auto* kernel = p.K % (2 * kStageK) == 0 ? mx4_tile_kernel<TM, TN, WM, WN, NBUF, EPI, kPairs>
+                   : p.K % kStageK == 0     ? mx4_tile_kernel<TM, TN, WM, WN, NBUF, EPI, kWordwise>
+                                          : mx4_tile_kernel<TM, TN, WM, WN, NBUF, EPI, kTail>;
     hipLaunchKernelGGL(kernel, dim3(gm * gn), block, 0, stream, p, gm, gn);
 }
 
@@ -752,13 +751,13 @@ hipError_t matmul_as(const Mx4Args& p, int src, hipStream_t stream)
         const int64_t t256 = ((p.M + 255) / 256) * ((p.N + 255) / 256);
         const int64_t t128 = ((p.M + 127) / 128) * ((p.N + 127) / 128);
         if (t256 >= 192)
-            tile_as<2, 4, 4, 2, 4, 2, EPI>(p, stream);
+            tile_as<2, 4, 4, 2, 2, EPI>(p, stream);
         else if (t128 > 256)
-            tile_as<2, 2, 2, 2, 4, 2, EPI>(p, stream);
+            tile_as<2, 2, 2, 2, 2, EPI>(p, stream);
         else if (t128 > 128)
-            tile_as<2, 2, 2, 2, 4, 3, EPI>(p, stream);
+            tile_as<2, 2, 2, 2, 3, EPI>(p, stream);
         else
-            tile_as<1, 1, 2, 2, 4, 3, EPI>(p, stream);
+            tile_as<1, 1, 2, 2, 3, EPI>(p, stream);
     }
     return hipGetLastError();
 }
