@@ -725,13 +725,9 @@ void few_as(const Mx4Args& p, hipStream_t stream)
 }
 
 template <int EPI>
-hipError_t matmul_as(const Mx4Args& p, int src, hipStream_t stream)
+hipError_t matmul_as(const Mx4Args& p, hipStream_t stream)
 {
-    if (src == 1) {
-        few_as<1, EPI>(p, stream);
-    } else if (src == 2) {
-        few_as<2, EPI>(p, stream);
-    } else if (p.M <= 16 || (p.M + 15) / 16 * ((p.N + 15) / 16) <= 512) {
+    if (p.M <= 16 || (p.M + 15) / 16 * ((p.N + 15) / 16) <= 512) {
         // As long as all workgroups of 16 x 16 are on the chip at once (two per
         // compute unit) they beat the tiles below, which then leave most of it
         // idle (us, against tiles of 64): 32 x 4096, K = 4096 5.9 / 7.5;
@@ -775,7 +771,7 @@ hipError_t launch_mx4_matmul(const Packed& a, const Packed& b, void* out, bool f
 {
     const Mx4Args p{(const uint8_t*)a.codes, a.scales, (const uint8_t*)b.codes, b.scales, out,
                     nullptr, nullptr, nullptr, nullptr, M, N, K};
-    return f32 ? matmul_as<kStoreF32>(p, 0, stream) : matmul_as<kStoreBf16>(p, 0, stream);
+    return f32 ? matmul_as<kStoreF32>(p, stream) : matmul_as<kStoreBf16>(p, stream);
 }
 
 hipError_t launch_mx4_matmul_fused(const void* a, bool a_f32, const Packed& b, void* out, bool f32,
@@ -783,8 +779,10 @@ hipError_t launch_mx4_matmul_fused(const void* a, bool a_f32, const Packed& b, v
 {
     const Mx4Args p{(const uint8_t*)a, nullptr, (const uint8_t*)b.codes, b.scales, out,
                     nullptr, nullptr, nullptr, nullptr, M, N, K};
-    const int src = a_f32 ? 2 : 1;
-    return f32 ? matmul_as<kStoreF32>(p, src, stream) : matmul_as<kStoreBf16>(p, src, stream);
+    auto* few = a_f32 ? (f32 ? few_as<2, kStoreF32> : few_as<2, kStoreBf16>)
+                      : (f32 ? few_as<1, kStoreF32> : few_as<1, kStoreBf16>);
+    few(p, stream);
+    return hipGetLastError();
 }
 
 hipError_t launch_mx4_write_back(const Packed& a, const Packed& b, const void* x,
@@ -793,7 +791,7 @@ hipError_t launch_mx4_write_back(const Packed& a, const Packed& b, const void* x
 {
     const Mx4Args p{(const uint8_t*)a.codes, a.scales, (const uint8_t*)b.codes, b.scales, f_out,
                     (const uint4*)x, Hpost, Hres, (uint4*)x_out, T, C, K};
-    return matmul_as<kWriteBack>(p, 0, stream);
+    return matmul_as<kWriteBack>(p, stream);
 }
 
 }  // namespace mhc
