@@ -904,15 +904,15 @@ hipError_t launch_layer_maps(const LayerPtrs& a, int64_t T, int64_t C, float eps
     return hipGetLastError();
 }
 
-hipError_t launch_layer_wt(const void* W, void* Wt, int64_t C, hipStream_t stream)
+static hipError_t launch_layer_wt(const void* W, void* Wt, int64_t C, hipStream_t stream)
 {
     hipLaunchKernelGGL(layer_wt_kernel, dim3((unsigned)((4 * C + kBlock - 1) / kBlock)), dim3(kBlock),
                        0, stream, (const uint16_t*)W, (uint4*)Wt, 4 * C);
     return hipGetLastError();
 }
 
-hipError_t launch_layer_dw_reduce(const float* partial, float* gW, int64_t C, int64_t groups,
-                                  hipStream_t stream)
+static hipError_t launch_layer_dw_reduce(const float* partial, float* gW, int64_t C, int64_t groups,
+                                         hipStream_t stream)
 {
     const int64_t n4 = (int64_t)kMaps * 4 * C / 4;
     hipLaunchKernelGGL(layer_dw_reduce_kernel, dim3((unsigned)((n4 + kBlock - 1) / kBlock)),

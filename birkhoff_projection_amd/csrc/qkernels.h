@@ -62,14 +62,10 @@ hipError_t launch_mx4_write_back(const Packed& a, const Packed& b, const void* x
                                  const float* Hpost, const float* Hres, void* x_out, void* f_out,
                                  int64_t T, int64_t C, int64_t K, hipStream_t stream);
 
-// Parts of the plain layer step (layer.hip) that the checkpointed one shares:
-// the maps pass of the forward, the transposition of W to [4C][24] bf16, and
-// the sum of the grad_W partials over the token groups.
+// The maps pass of the plain layer's forward (layer.hip), which the checkpointed
+// step and the read half share.
 hipError_t launch_layer_maps(const LayerPtrs& a, int64_t T, int64_t C, float eps,
                              const SolverOpts& o, hipStream_t stream);
-hipError_t launch_layer_wt(const void* W, void* Wt, int64_t C, hipStream_t stream);
-hipError_t launch_layer_dw_reduce(const float* partial, float* gW, int64_t C, int64_t groups,
-                                  hipStream_t stream);
 
 // The read half of the layer step: a.rms .. a.H_res, and u as bf16 (a.u) and /
 // or MXFP4 (u4), each if its pointer is not NULL.  a.workspace holds
