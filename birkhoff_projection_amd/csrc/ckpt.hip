@@ -8,12 +8,16 @@
 //   mix backward       grad_x_j = sum_i H_ij g_i, grad_H_ij = <g_i, xhat_j>
 //                      with xhat the packed x
 //
-// All of them stream each byte once and are bound by HBM; a lane moves 8
-// columns (16 bytes of bf16, 8 or 4 bytes of codes), consecutive lanes take
-// consecutive columns.  Measured: pack and unpack 65536 x 7168 221 and 228 us
-// (6.3 TB/s), 4-bit rows of 16384 x 7168 46 us, columns 53-60 (5 TB/s), both
-// 90, columns from a checkpoint 42; mix 16384 x 4096 forward 240 us, backward
-// 246 (5.5 TB/s).
+// All of them move each byte once; a lane moves 8 columns (16 bytes of bf16, 8
+// or 4 bytes of codes), consecutive lanes take consecutive columns.  Along the
+// rows they are bound by HBM: pack and unpack 65536 x 7168 221 and 228 us
+// (6.3 TB/s), 4-bit rows of 16384 x 7168 46 us, of 8192 x 4096 15 (5.7 TB/s);
+// mix 16384 x 4096 forward 240 us, backward 246 (5.5 TB/s).  Along the columns
+// 16384 x 7168 takes 53-60 us (5 TB/s), both 90, columns from a checkpoint 42
+// (4.4), but few tiles do not reach that rate: columns of 8192 x 4096 26 us
+// (3.2 TB/s), both of 8192 x 8192 57 (3.6), from a checkpoint 8192 x 4096 18
+// (2.9).  A tile's workgroup loads all, then stores all, and there is little
+// more than one round of workgroups to overlap the two.
 #include "mxfmt.h"
 #include "proj4.h"
 #include "qkernels.h"

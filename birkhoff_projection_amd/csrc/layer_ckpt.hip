@@ -708,7 +708,7 @@ __global__ __launch_bounds__(kBlock) __attribute__((amdgpu_waves_per_eu(2))) voi
 //   dW^T tile (32 maps x 16 k) += dlT (32 maps x 32 tokens) * xhat (32 tokens x 16 k)
 // Chunks of 32 tokens are copied straight from memory to LDS, two chunks ahead
 // (with the loads in registers, one ahead, two waves per SIMD did not hide
-// them: 16384 x 7168 162 us, so 112, the codes at 4.2 TB/s): a wave its own columns' codes and scales, all four the chunk's dlT,
+// them: 16384 x 7168 162 us, so 112-120, the codes at 3.9-4.2 TB/s): a wave its own columns' codes and scales, all four the chunk's dlT,
 // which lies together.  One barrier per chunk.
 //
 // The MFMA B operand wants 8 consecutive tokens of one k per lane, the memory

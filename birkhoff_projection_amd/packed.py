@@ -129,7 +129,7 @@ def projected_mix(x, logits, *, format="e4m3", **opts):
     [T,4,4] fp32.  Keeps H and an 8-bit checkpoint of x; the gradient for the
     logits is that of the checkpointed x.  ``opts`` are the solver's.  A
     captured backward raises where it would reach an eager graph on the default
-    stream."""
+    stream, at x or logits or behind their casts and views."""
     return ProjectedMix.apply(x, logits, format, opts)
 
 
@@ -283,8 +283,10 @@ def mx4_linear(x, w, *, format="e4m3"):
     N and K multiples of 32).  Each of the three products takes both operands
     in MXFP4, quantised along the axis it sums over: y = q(x) q(w)^T,
     grad_x = q(gy) q(w^T)^T, grad_w = q(gy^T) q(xhat^T)^T.  x is kept for the
-    backward as an 8-bit checkpoint (xhat), w as it is.  Differentiable once; a captured
-    backward raises where it would reach an eager graph on the default stream."""
+    backward as an 8-bit checkpoint (xhat), w as it is, whichever gradients are
+    wanted; without any, mx4_matmul of a quantised w does less.  Differentiable once.
+    A captured backward raises where it would reach an eager graph on the
+    default stream, at w or x or behind their casts and views."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be [M, K] and [N, K]")
     if any(s % BLOCK for s in (*x.shape, *w.shape)):
